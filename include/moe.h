@@ -89,7 +89,9 @@ enum moe_status_code {
     MOE_ERR_TIMEOUT = 6,             /* device: a bounded wait ran out           */
     MOE_ERR_MISALIGNED = 7,          /* a pointer is not 16-byte aligned         */
     MOE_ERR_NO_DEVICE = 8,           /* no usable sm_100-family device           */
-    MOE_ERR_STATIC_SCRATCH_LIMIT = 9 /* shape needs more than the static scratch */
+    MOE_ERR_STATIC_SCRATCH_LIMIT = 9, /* shape needs more than the static scratch */
+    MOE_ERR_BAD_INDEX = 10           /* device: an offset, length, position, slot or page out of
+                                      * range (moe_attention.h) */
 };
 
 enum moe_workspace_kind {

@@ -1,4 +1,5 @@
-"""ctypes binding of libmoe_gb300.so (include/moe.h), argument marshalling only.
+"""ctypes binding of libmoe_gb300.so (include/moe.h, include/moe_attention.h),
+argument marshalling only.
 
 Every function here has the name of the C entry point it calls, takes torch
 tensors (device tensors for the compute calls) and passes their data pointers
@@ -25,6 +26,7 @@ MOE_ERR_TIMEOUT = 6
 MOE_ERR_MISALIGNED = 7
 MOE_ERR_NO_DEVICE = 8
 MOE_ERR_STATIC_SCRATCH_LIMIT = 9
+MOE_ERR_BAD_INDEX = 10
 MOE_NOALLOC_DISPATCH_MAX_ENTRIES = 1 << 20
 
 MOE_WS_ROUTE, MOE_WS_DISPATCH, MOE_WS_FORWARD, MOE_WS_BACKWARD = 0, 1, 2, 3
@@ -42,6 +44,35 @@ class MoeShape(ctypes.Structure):
 class MoeKernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int32),
                 ("total_ms", ctypes.c_double)]
+
+
+MOE_ROPE_HALF, MOE_ROPE_INTERLEAVED = 0, 1
+ROPE_LAYOUTS = {"half": MOE_ROPE_HALF, "interleaved": MOE_ROPE_INTERLEAVED}
+
+
+class MoeAttnShape(ctypes.Structure):
+    _fields_ = [("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32)]
+
+
+class MoeHeads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class MoeRope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_int32),
+                ("dims", ctypes.c_int32), ("layout", ctypes.c_int32)]
+
+
+class MoeKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
+
+
+class MoePacked(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Tq", ctypes.c_int32), ("Tk", ctypes.c_int32),
+                ("max_q", ctypes.c_int32), ("max_k", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p)]
 
 
 class MoeError(RuntimeError):
@@ -75,6 +106,24 @@ def _load() -> ctypes.CDLL:
         "moe_workspace_size_rows": (S, [MoeShape, ctypes.c_int32, I]),
         "moe_forward_rows": (I, [MoeShape, ctypes.c_int32] + [P] * 13 + [S, P]),
         "moe_backward_rows": (I, [MoeShape, ctypes.c_int32] + [P] * 20 + [S, P]),
+        "moe_rope_table": (I, [ctypes.c_int32, ctypes.c_int32, P, ctypes.c_double, P, P]),
+        "moe_norm_rope": (I, [MoeAttnShape, ctypes.c_int32, MoeHeads, MoeHeads, P, P,
+                              ctypes.c_float, P, MoeRope, MoeHeads, MoeHeads, P]),
+        "moe_norm_rope_workspace_size": (S, [MoeAttnShape, ctypes.c_int32]),
+        "moe_norm_rope_backward": (I, [MoeAttnShape, ctypes.c_int32] + [MoeHeads] * 4 +
+                                   [P, P, ctypes.c_float, P, MoeRope, MoeHeads, MoeHeads, P, P,
+                                    P, S, P]),
+        "moe_kv_append": (I, [MoeAttnShape, ctypes.c_int32] + [MoeHeads] * 3 +
+                          [P, P, ctypes.c_float, P, MoeRope, P, MoeHeads, MoeKvCache, P]),
+        "moe_attention_forward": (I, [MoeAttnShape, MoePacked, ctypes.c_float] + [MoeHeads] * 4 +
+                                  [P, P]),
+        "moe_attention_backward_workspace_size": (S, [MoeAttnShape, MoePacked]),
+        "moe_attention_backward": (I, [MoeAttnShape, MoePacked, ctypes.c_float] + [MoeHeads] * 5 +
+                                   [P] + [MoeHeads] * 3 + [P, S, P]),
+        "moe_attention_decode_workspace_size": (S, [MoeAttnShape] + [ctypes.c_int32] * 3),
+        "moe_attention_decode": (I, [MoeAttnShape] + [ctypes.c_int32] * 3 +
+                                 [ctypes.c_float, MoeHeads, MoeKvCache, P, ctypes.c_int32, P,
+                                  MoeHeads, P, S, P]),
         "moe_get_error": (I, [P]),
         "moe_selftest_bounded_wait": (I, [ctypes.c_uint64, P]),
         "moe_status_string": (ctypes.c_char_p, [I]),
@@ -269,3 +318,89 @@ def moe_timing_collect() -> dict:
         raise MoeError(-n, "moe_timing_collect")
     return {buf[i].name.decode(): (int(buf[i].launches), float(buf[i].total_ms))
             for i in range(min(n, 64))}
+
+
+# ------------------------------------------------------- attention (moe_attention.h)
+def heads(t) -> MoeHeads:
+    """The view of a bf16 tensor [T, H, D] (any token and head strides); None: no data."""
+    if t is None:
+        return MoeHeads(None, 0, 0)
+    st = t.stride()
+    return MoeHeads(t.data_ptr(), st[0], st[1])
+
+
+def moe_rope_table(positions, dims, inv_freq, scale, table, stream=None, check=True):
+    rc = LIB.moe_rope_table(positions, dims, _ptr(inv_freq), scale, _ptr(table), _stream(stream))
+    if check:
+        _check(rc, "moe_rope_table")
+    return rc
+
+
+def moe_norm_rope(a, T, q, k, wq, wk, eps, positions, rope, q_out, k_out, stream=None,
+                  check=True):
+    rc = LIB.moe_norm_rope(a, T, heads(q), heads(k), _ptr(wq), _ptr(wk), eps, _ptr(positions),
+                           rope, heads(q_out), heads(k_out), _stream(stream))
+    if check:
+        _check(rc, "moe_norm_rope")
+    return rc
+
+
+def moe_norm_rope_workspace_size(a, T) -> int:
+    return int(LIB.moe_norm_rope_workspace_size(a, T))
+
+
+def moe_norm_rope_backward(a, T, dq_out, dk_out, q, k, wq, wk, eps, positions, rope, dq, dk, dwq,
+                           dwk, ws, stream=None, check=True):
+    rc = LIB.moe_norm_rope_backward(a, T, heads(dq_out), heads(dk_out), heads(q), heads(k),
+                                    _ptr(wq), _ptr(wk), eps, _ptr(positions), rope, heads(dq),
+                                    heads(dk), _ptr(dwq), _ptr(dwk), _ptr(ws), _nbytes(ws),
+                                    _stream(stream))
+    if check:
+        _check(rc, "moe_norm_rope_backward")
+    return rc
+
+
+def moe_kv_append(a, T, q, k, v, wq, wk, eps, positions, rope, slots, q_out, cache, stream=None,
+                  check=True):
+    rc = LIB.moe_kv_append(a, T, heads(q), heads(k), heads(v), _ptr(wq), _ptr(wk), eps,
+                           _ptr(positions), rope, _ptr(slots), heads(q_out), cache,
+                           _stream(stream))
+    if check:
+        _check(rc, "moe_kv_append")
+    return rc
+
+
+def moe_attention_forward(a, s, scale, q, k, v, out, lse, stream=None, check=True):
+    rc = LIB.moe_attention_forward(a, s, scale, heads(q), heads(k), heads(v), heads(out),
+                                   _ptr(lse), _stream(stream))
+    if check:
+        _check(rc, "moe_attention_forward")
+    return rc
+
+
+def moe_attention_backward_workspace_size(a, s) -> int:
+    return int(LIB.moe_attention_backward_workspace_size(a, s))
+
+
+def moe_attention_backward(a, s, scale, dout, q, k, v, out, lse, dq, dk, dv, ws, stream=None,
+                           check=True):
+    rc = LIB.moe_attention_backward(a, s, scale, heads(dout), heads(q), heads(k), heads(v),
+                                    heads(out), _ptr(lse), heads(dq), heads(dk), heads(dv),
+                                    _ptr(ws), _nbytes(ws), _stream(stream))
+    if check:
+        _check(rc, "moe_attention_backward")
+    return rc
+
+
+def moe_attention_decode_workspace_size(a, batch, n, max_kv) -> int:
+    return int(LIB.moe_attention_decode_workspace_size(a, batch, n, max_kv))
+
+
+def moe_attention_decode(a, batch, n, max_kv, scale, q, cache, block_table, table_stride, kv_lens,
+                         out, ws, stream=None, check=True):
+    rc = LIB.moe_attention_decode(a, batch, n, max_kv, scale, heads(q), cache, _ptr(block_table),
+                                  table_stride, _ptr(kv_lens), heads(out), _ptr(ws), _nbytes(ws),
+                                  _stream(stream))
+    if check:
+        _check(rc, "moe_attention_decode")
+    return rc

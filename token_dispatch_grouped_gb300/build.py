@@ -36,7 +36,7 @@ def nvcc() -> str:
 def _sources():
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     deps = srcs + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
-        [os.path.join(ROOT, "include", "moe.h")]
+        sorted(glob.glob(os.path.join(ROOT, "include", "*.h")))
     return srcs, deps
 
 

@@ -894,6 +894,8 @@ const char* moe_status_string(int status) {
         case MOE_ERR_NO_DEVICE: return "no usable CUDA device";
         case MOE_ERR_STATIC_SCRATCH_LIMIT:
             return "shape needs more scratch than the library's static device array holds";
+        case MOE_ERR_BAD_INDEX:
+            return "sequence offset, length, position, slot or page out of range";
     }
     return "unknown status";
 }
