@@ -12,6 +12,7 @@
 #include <string>
 #include <vector>
 
+#include "attn_mma.cuh"
 #include "common.cuh"
 
 namespace moe {
@@ -395,6 +396,23 @@ bool make_tmap_f32(CUtensorMap* map, const void* base, uint64_t rows, uint64_t c
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
+
+namespace attn {
+bool make_tmap_heads(CUtensorMap* map, const Heads& h, int T, int H, int D, uint32_t box_heads,
+                     uint32_t box_tokens) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
+                          static_cast<cuuint64_t>(T)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(h.hs) * 2, static_cast<cuuint64_t>(h.ts) * 2};
+    cuuint32_t box[3] = {64, box_heads, box_tokens};
+    cuuint32_t es[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, h.p, dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace attn
 
 int* device_status_word() { return status_ptr(); }
 
