@@ -1,158 +1,644 @@
 // attention_bwd.cu — the backward of softmax attention over packed sequences.
 //
-//   S = scale q k^T, lse = log sum_j exp S_j, P = exp(S - lse), out = P v;
-//   dP = dout v^T, delta = sum_i dout_i out_i, dS = P (dP - delta),
-//   dv = P^T dout, dq = scale dS k, dk = scale dS^T q.
+//   P = exp(scale q k^T - lse),  delta = sum_i dout_i out_i,  dP = dout v^T,
+//   dS = P (dP - delta),  dq = scale dS k,  dk = scale dS^T q,  dv = P^T dout.
 //
-// One warp per row (of q, or of k and v for their gradients): the lanes take 32 rows
-// of the other side at a time for the dot products, then 4 of the D columns each for
-// the weighted sums, in one pass with a running maximum and sum.
-#include "attn.cuh"
+// Two kernels, so that every gradient is summed by one CTA in one order (a single kernel
+// over key tiles would need atomics, or fp32 partials of dq larger than all other
+// traffic). The scores and dP are formed in both: 7 products against the least 5.
+//   dq_kernel   a tile of 128 query rows (the G heads of 128 / G tokens) over its key
+//               tiles: S = Q K^T, dP = dO V^T, dQ += dS K. It also writes delta and lse of
+//               its rows in tile order for the second kernel.
+//   dkv_kernel  a tile of 128 keys over the query tiles that see it, transposed so that
+//               keys are rows: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.
+//               The G heads of a group are rows of the same tiles, so their sum is the
+//               product's.
+// Roles as in the forward: a TMA warp, a warp that issues the tcgen05 products, and two
+// groups of four warps that turn scores into weights, each for 64 of the 128 columns of
+// every row; P and dS go back to TMEM as bf16 operands over the columns that their group
+// has read. The order of the products (dP, [P] dV, next S, [dS] dK) leaves the tensor
+// cores work while the other warps compute: P while dP runs, dS while dV and the next S
+// run. TMEM: dq_kernel S twice, dP, dQ; dkv_kernel S, dP, dV, dK (4 x 128 columns).
+//
+// P and dS are rounded to bf16 (the operand type), everything else is fp32; scale enters
+// dq and dk once at the end. Masked weights are zero by selection, and rows of an operand
+// that lie past the sequence are zeroed in shared memory where they are summed over.
+#include "attn_mma.cuh"
 
 namespace moe {
 namespace attn {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kMaxD = 128;
+constexpr int kThreads = 384;   // 8 compute warps, tensor cores, TMA, row data, (idle)
+constexpr int kCompute = 256;
+constexpr float kLog2e = 1.44269504088896341f;
 
-// The sequence of packed row t (offsets cu, `rows` of them at most), or false.
-__device__ bool find(const int32_t* cu, int B, int t, int& b) {
-    int lo = 0, hi = B;  // last b with cu[b] <= t
-    while (hi - lo > 1) {
-        const int m = (lo + hi) >> 1;
-        if (cu[m] <= t) lo = m;
-        else hi = m;
-    }
-    b = lo;
-    return t >= cu[lo] && t < cu[lo + 1];
+struct Params {
+    moe_attn_shape a;
+    Packed s;
+    float scale;
+    Heads out, dout, dq, dk, dv;
+    const float* lse;
+    float *row_lse, *row_delta;  // [Hkv][Tq][G]: lse * log2(e) (+inf: no key) and delta
+    int* err;
+    int tpt;  // tokens of a 128-row query tile
+};
+
+template <int DP>
+struct Cfg {
+    static constexpr int PIECES = DP / 64;
+    static constexpr int TILE = PIECES * kPiece;
+    static constexpr int R0 = 3, R1 = 2;  // ring stages: the operand used twice, the other
+    static constexpr int TILES = (2 + R0 + R1) * TILE;
+    static constexpr int SMEM_Q = TILES + 2 * 512 + 256;       // delta halves, barriers
+    static constexpr int SMEM_KV = TILES + 2 * 2 * 512 + 256;  // two slots of lse and delta
+};
+
+// 64 columns of TMEM as fp32.
+__device__ __forceinline__ void load64(uint32_t t, float (&v)[64]) {
+    tmem_ld32(t, *reinterpret_cast<uint32_t(*)[32]>(v));
+    tmem_ld32(t + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+    tmem_ld_wait();
 }
-
-// One warp of the grid looks all sequences over.
-__device__ void check_sequences(const Packed& s, int lane, int* err) {
-    int q0, nq, k0, nk;
-    for (int b = lane; b < s.B; b += 32) sequence_of(s, b, q0, nq, k0, nk, err);
-}
-
-__device__ __forceinline__ float dot(const float* q, const bf16* row, int D) {
-    float s = 0.f;
-    for (int i = 0; i < D; i += 8) {
-        float v[8];
-        unpack8(*reinterpret_cast<const uint4*>(row + i), v);
+// 64 fp32 values as 32 columns of bf16 pairs.
+__device__ __forceinline__ void store64(uint32_t t, const float (&v)[64]) {
+    uint32_t w[32];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s += q[i + e] * v[e];
-    }
-    return s;
+    for (int i = 0; i < 32; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1]);
+    tmem_st32(t, w);
+    tmem_st_wait();
+}
+// k-th 16 columns of a bf16 operand that the two groups wrote: group 0's 64 columns at
+// t, group 1's at t + 64 (over the scores that each of them read).
+__device__ __forceinline__ uint32_t operand(uint32_t t, int k) {
+    return t + (k < 4 ? 8 * k : 64 + 8 * (k - 4));
 }
 
-__device__ __forceinline__ void stage(float* dst, const bf16* row, int D, int lane) {
-    __syncwarp();
-    for (int i = lane; i < D; i += 32) dst[i] = __bfloat162float(row[i]);
-    __syncwarp();
-}
-
-// delta and dq of one query row.
-__global__ void __launch_bounds__(kWarps * 32) dq_kernel(const Attention p) {
-    __shared__ float s_q[kWarps][kMaxD], s_do[kWarps][kMaxD];
-    pdl_wait();
-    pdl_trigger();
-    if (has_error(p.err)) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (blockIdx.x == 0 && warp == 0) check_sequences(p.s, lane, p.err);
-    const int Hq = p.a.Hq, D = p.a.D;
-    const long long row = static_cast<long long>(blockIdx.x) * kWarps + warp;
-    if (row >= static_cast<long long>(p.s.Tq) * Hq) return;
-    const int t = static_cast<int>(row / Hq), h = static_cast<int>(row % Hq);
-    const int hk = h / (Hq / p.a.Hkv);
-    int b, q0, nq, k0, nk;
-    if (!find(p.s.cu_q, p.s.B, t, b) || !sequence_of(p.s, b, q0, nq, k0, nk, p.err)) return;
-    stage(s_q[warp], p.q.row(t, h), D, lane);
-    stage(s_do[warp], p.dout.row(t, h), D, lane);
-    float delta = 0.f;
-    for (int i = lane; i < D; i += 32) delta += s_do[warp][i] * __bfloat162float(p.out.row(t, h)[i]);
-    for (int o = 16; o > 0; o >>= 1) delta += __shfl_xor_sync(~0u, delta, o);
-    if (lane == 0) p.delta[row] = delta;
-    const float lse = p.lse[row];
-    const int seen = lse == -INFINITY ? 0 : p.s.causal ? min(nk, t - q0 + nk - nq + 1) : nk;
-    float acc[kMaxD / 32] = {};
-    for (int j0 = 0; j0 < seen; j0 += 32) {
-        const int j = j0 + lane;
-        float ds = 0.f;
-        if (j < seen) {
-            const float w = __expf(p.scale * dot(s_q[warp], p.k.row(k0 + j, hk), D) - lse);
-            ds = w * (dot(s_do[warp], p.v.row(k0 + j, hk), D) - delta);
+// 32 rows x W columns (fp32, TMEM columns t ..) of one warp, times f, as bf16 rows:
+// row(r) gives the row's destination or nullptr. stg: 32 x W x 2 bytes of shared memory.
+template <int W, class Row>
+__device__ __forceinline__ void store_rows(uint32_t t, bool any, float f, uint8_t* stg, int lane,
+                                           int col0, int D, Row row) {
+    constexpr int CH = W / 8;
+#pragma unroll
+    for (int q = 0; q < W; q += 32) {
+        uint32_t o[32];
+        if (any) {
+            tmem_ld32(t + q, o);
+            tmem_ld_wait();
         }
-        for (int i = 0; i < min(32, seen - j0); ++i) {
-            const float di = __shfl_sync(~0u, ds, i);
-            const bf16* k = p.k.row(k0 + j0 + i, hk);
-            for (int c = 0; c < kMaxD / 32; ++c)
-                if (c * 32 + lane < D) acc[c] += di * __bfloat162float(k[c * 32 + lane]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = any ? __uint_as_float(o[8 * i + e]) * f : 0.f;
+            *reinterpret_cast<uint4*>(stg + lane * W * 2 + ((q / 8 + i) ^ (lane & (CH - 1))) * 16) =
+                pack8(v);
         }
     }
-    for (int c = 0; c < kMaxD / 32; ++c)
-        if (c * 32 + lane < D) p.dq.row(t, h)[c * 32 + lane] = __float2bfloat16(p.scale * acc[c]);
+    __syncwarp();
+    constexpr int RPI = 32 / CH;
+#pragma unroll 4
+    for (int i = 0; i < 32; i += RPI) {
+        const int rl = i + lane / CH, ch = lane % CH;
+        bf16* dst = row(rl);
+        if (dst != nullptr && col0 + ch * 8 < D)
+            *reinterpret_cast<uint4*>(dst + col0 + ch * 8) =
+                *reinterpret_cast<const uint4*>(stg + rl * W * 2 + (ch ^ (rl & (CH - 1))) * 16);
+    }
 }
 
-// dk and dv of one key row, over the queries that see it in each head of its group.
-__global__ void __launch_bounds__(kWarps * 32) dkv_kernel(const Attention p) {
-    __shared__ float s_k[kWarps][kMaxD], s_v[kWarps][kMaxD];
+// ---------------------------------------------------------------------- dq
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapDO,
+          const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+          const Params p) {
+    using C = Cfg<DP>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sQ = smem_u32(smem), sDO = sQ + C::TILE;
+    const uint32_t sK = sDO + C::TILE, sV = sK + C::R0 * C::TILE;
+    float* half_delta = reinterpret_cast<float*>(smem + C::TILES);  // [2][128]
+    uint8_t* misc = smem + C::TILES + 1024;
+    const uint32_t bars = smem_u32(misc);
+    const auto k_full = [&](int s) { return bars + 8u * s; };
+    const auto k_empty = [&](int s) { return bars + 8u * (3 + s); };
+    const auto v_full = [&](int s) { return bars + 8u * (6 + s); };
+    const auto v_empty = [&](int s) { return bars + 8u * (8 + s); };
+    const auto s_bar = [&](int s) { return bars + 8u * (10 + s); };
+    const uint32_t q_bar = bars + 96, do_bar = bars + 104, dp_bar = bars + 112,
+                   ds_bar = bars + 120, done_bar = bars + 128;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 136);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* found = reinterpret_cast<int*>(tmem_slot + 2);
+    constexpr uint32_t TM_S = 0, TM_DP = 256, TM_DQ = 384;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 12; ++i) mbar_init(bars + 8 * i, 1);
+        mbar_init(q_bar, 1);
+        mbar_init(do_bar, 1);
+        mbar_init(dp_bar, 1);
+        mbar_init(ds_bar, kCompute);
+        mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
     pdl_wait();
     pdl_trigger();
-    if (has_error(p.err)) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int Hq = p.a.Hq, Hkv = p.a.Hkv, D = p.a.D, G = Hq / Hkv;
-    const long long row = static_cast<long long>(blockIdx.x) * kWarps + warp;
-    if (row >= static_cast<long long>(p.s.Tk) * Hkv) return;
-    const int t = static_cast<int>(row / Hkv), hk = static_cast<int>(row % Hkv);
-    int b, q0, nq, k0, nk;
-    if (!find(p.s.cu_k, p.s.B, t, b) || !sequence_of(p.s, b, q0, nq, k0, nk, p.err)) return;
-    stage(s_k[warp], p.k.row(t, hk), D, lane);
-    stage(s_v[warp], p.v.row(t, hk), D, lane);
-    const int first = p.s.causal ? max(0, t - k0 + nq - nk) : 0;
-    float ak[kMaxD / 32] = {}, av[kMaxD / 32] = {};
-    for (int g = 0; g < G; ++g) {
-        const int h = hk * G + g;
-        for (int i0 = first; i0 < nq; i0 += 32) {
-            const int i = q0 + i0 + lane;
-            float w = 0.f, ds = 0.f;
-            if (i0 + lane < nq) {
-                const long long r = static_cast<long long>(i) * Hq + h;
-                w = __expf(p.scale * dot(s_k[warp], p.q.row(i, h), D) - p.lse[r]);
-                ds = w * (dot(s_v[warp], p.dout.row(i, h), D) - p.delta[r]);
-            }
-            for (int u = 0; u < min(32, nq - i0); ++u) {
-                const float wu = __shfl_sync(~0u, w, u), du = __shfl_sync(~0u, ds, u);
-                const bf16 *q = p.q.row(q0 + i0 + u, h), *dd = p.dout.row(q0 + i0 + u, h);
-                for (int c = 0; c < kMaxD / 32; ++c)
-                    if (c * 32 + lane < D) {
-                        av[c] += wu * __bfloat162float(dd[c * 32 + lane]);
-                        ak[c] += du * __bfloat162float(q[c * 32 + lane]);
+    const int hk = blockIdx.y, tpt = p.tpt, G = p.a.Hq / p.a.Hkv;
+    if (warp == 0) {
+        int b = -1, item = 0, items = 0;
+        if ((sQ & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
+        const bool skip = __any_sync(~0u, has_error(p.err));
+        if (skip || !find_tile(p.s, false, tpt, blockIdx.x, lane, b, item, items, p.err)) b = -1;
+        if (lane == 0) {
+            found[0] = b;
+            found[1] = items - 1 - item;  // the longest rows of a sequence first
+        }
+    }
+    if (warp == 1 && blockIdx.x == 0 && hk == 0) check_sequences(p.s, lane, p.err);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int b = found[0];
+    if (b >= 0) {
+        const int q0 = p.s.cu_q[b], nq = p.s.cu_q[b + 1] - q0;
+        const int k0 = p.s.cu_k[b], nk = p.s.cu_k[b + 1] - k0;
+        const int first = found[1] * tpt;
+        const int seen = p.s.causal ? max(0, min(nk, min(first + tpt, nq) + nk - nq)) : nk;
+        const int n = (seen + kRows - 1) / kRows;
+
+        if (warp == 9) {
+            if (lane == 0 && n > 0) {
+                const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int h, int t) {
+                    for (int c = 0; c < C::PIECES; ++c)
+                        tma_load_3d(dst + c * kPiece, m, bar, 64 * c, h, t);
+                };
+                const uint32_t qbytes = C::PIECES * 128 * G * tpt;
+                mbar_arrive_expect_tx(q_bar, qbytes);
+                load(sQ, &mapQ, q_bar, hk * G, q0 + first);
+                int jk = 0, jv = 0;
+                for (int j = 0; j < n; ++j) {
+                    int s = j % C::R0;
+                    if (j >= C::R0 && !mbar_wait(k_empty(s), (j / C::R0 - 1) & 1, abort_flag, kWaitNs))
+                        break;
+                    mbar_arrive_expect_tx(k_full(s), C::TILE);
+                    load(sK + s * C::TILE, &mapK, k_full(s), hk, k0 + j * kRows);
+                    ++jk;
+                    if (j == 0) {
+                        mbar_arrive_expect_tx(do_bar, qbytes);
+                        load(sDO, &mapDO, do_bar, hk * G, q0 + first);
                     }
+                    s = j % C::R1;
+                    if (j >= C::R1 && !mbar_wait(v_empty(s), (j / C::R1 - 1) & 1, abort_flag, kWaitNs))
+                        break;
+                    mbar_arrive_expect_tx(v_full(s), C::TILE);
+                    load(sV + s * C::TILE, &mapV, v_full(s), hk, k0 + j * kRows);
+                    ++jv;
+                }
+                // nothing is in flight when the CTA leaves
+                drain(q_bar, 0);
+                drain(do_bar, 0);
+                for (int j = max(0, jk - C::R0); j < jk; ++j) drain(k_full(j % C::R0), (j / C::R0) & 1);
+                for (int j = max(0, jv - C::R1); j < jv; ++j) drain(v_full(j % C::R1), (j / C::R1) & 1);
+            }
+        } else if (warp == 8) {
+            const int ksteps = (p.a.D + 15) / 16;
+            const uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_q = idesc_bf16(128, 16 * ksteps, 0, 1);
+            // S_j, once its keys are there
+            const auto scores = [&](int j) -> bool {
+                const int s = j % C::R0;
+                if (!warp_wait(k_full(s), (j / C::R0) & 1, abort_flag)) return false;
+                if (seen - j * kRows < kRows)
+                    zero_tail(sK + s * C::TILE, C::PIECES, seen - j * kRows, lane);
+                tc_fence_after();
+                if (lane == 0) {
+                    for (int k = 0; k < ksteps; ++k)
+                        mma_bf16(tmem + TM_S + 128 * (j & 1), desc_k(sQ, k),
+                                 desc_k(sK + s * C::TILE, k), id_s, k > 0);
+                    mma_commit(s_bar(j & 1));
+                }
+                __syncwarp();
+                return true;
+            };
+            bool ok = n == 0 || (warp_wait(q_bar, 0, abort_flag) && scores(0) &&
+                                 warp_wait(do_bar, 0, abort_flag));
+            for (int j = 0; j < n && ok; ++j) {
+                const int sv = j % C::R1, sk = j % C::R0;
+                ok = warp_wait(v_full(sv), (j / C::R1) & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    for (int k = 0; k < ksteps; ++k)
+                        mma_bf16(tmem + TM_DP, desc_k(sDO, k), desc_k(sV + sv * C::TILE, k), id_s,
+                                 k > 0);
+                    mma_commit(dp_bar);
+                    mma_commit(v_empty(sv));
+                }
+                __syncwarp();
+                if (j + 1 < n) ok = scores(j + 1);
+                ok = ok && warp_wait(ds_bar, j & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    for (int k = 0; k < kRows / 16; ++k)
+                        mma_bf16_ta(tmem + TM_DQ, operand(tmem + TM_DP, k),
+                                    desc_mn(sK + sk * C::TILE, k), id_q, (j | k) != 0);
+                    mma_commit(k_empty(sk));
+                }
+                __syncwarp();
+            }
+            if (lane == 0) {
+                mma_commit(done_bar);
+                drain(done_bar, 0);
+            }
+            __syncwarp();
+        } else if (warp < 8) {
+            const int grp = warp >> 2, row = threadIdx.x & 127;
+            const int token = first + row / G, g = row % G;
+            const bool valid = row < G * tpt && token < nq;
+            const int mine = !valid ? 0 : p.s.causal ? min(nk, token + 1 + nk - nq) : nk;
+            const int open = p.s.causal ? first + 1 + nk - nq : nk;  // keys that every row sees
+            const float c = p.scale * kLog2e;
+            const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+            // delta: each group sums half of the row's columns
+            float delta = 0.f, lse2 = INFINITY;
+            if (valid) {
+                const bf16* o = p.out.row(q0 + token, hk * G + g);
+                const bf16* d = p.dout.row(q0 + token, hk * G + g);
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i) {
+                    const int col = grp * (DP / 2) + i * 8;
+                    if (col >= p.a.D) break;
+                    float x[8], y[8];
+                    unpack8(*reinterpret_cast<const uint4*>(o + col), x);
+                    unpack8(*reinterpret_cast<const uint4*>(d + col), y);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) delta += x[e] * y[e];
+                }
+                const float e = p.lse[static_cast<long long>(q0 + token) * p.a.Hq + hk * G + g];
+                lse2 = e == -INFINITY ? INFINITY : e * kLog2e;
+            }
+            half_delta[grp * 128 + row] = delta;
+            asm volatile("bar.sync 1, %0;" ::"n"(kCompute) : "memory");
+            delta = half_delta[row] + half_delta[128 + row];
+            if (valid && grp == 0) {
+                const long long at = (static_cast<long long>(hk) * p.s.Tq + q0 + token) * G + g;
+                p.row_lse[at] = lse2;
+                p.row_delta[at] = delta;
+            }
+            bool ok = true;
+            for (int j = 0; j < n; ++j) {
+                ok = warp_wait(s_bar(j & 1), (j >> 1) & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                float s[64], d[64];
+                load64(lanes + TM_S + 128 * (j & 1) + 64 * grp, s);
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) {
+                    fma2(s[i], s[i + 1], s[i], s[i + 1], c, -lse2);
+                    s[i] = exp2_fast(s[i]);
+                    s[i + 1] = exp2_fast(s[i + 1]);
+                }
+                ok = warp_wait(dp_bar, j & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                load64(lanes + TM_DP + 64 * grp, d);
+#pragma unroll
+                for (int i = 0; i < 64; ++i) d[i] = s[i] * (d[i] - delta);
+                if ((j + 1) * kRows > open) {
+                    const int lim = mine - j * kRows - 64 * grp;
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) d[i] = i < lim ? d[i] : 0.f;
+                }
+                store64(lanes + TM_DP + 64 * grp, d);
+                tc_fence_before();
+                mbar_arrive(ds_bar);
+            }
+            if (ok && n > 0) ok = mbar_wait(done_bar, 0, abort_flag, kWaitNs);
+            ok = __all_sync(~0u, ok);
+            if (ok) {
+                tc_fence_after();
+                constexpr int W = DP / 2;
+                store_rows<W>(lanes + TM_DQ + grp * W, n > 0, p.scale,
+                              smem + warp * 32 * W * 2, lane, grp * W, p.a.D, [&](int r) -> bf16* {
+                                  const int rr = (warp & 3) * 32 + r, t = first + rr / G;
+                                  return rr < G * tpt && t < nq ? p.dq.row(q0 + t, hk * G + rr % G)
+                                                                : nullptr;
+                              });
             }
         }
     }
-    for (int c = 0; c < kMaxD / 32; ++c)
-        if (c * 32 + lane < D) {
-            p.dk.row(t, hk)[c * 32 + lane] = __float2bfloat16(p.scale * ak[c]);
-            p.dv.row(t, hk)[c * 32 + lane] = __float2bfloat16(av[c]);
-        }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (threadIdx.x == 0 && *abort_flag) raise_error(p.err, MOE_ERR_TIMEOUT);
+    if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-dim3 row_grid(long long rows) { return dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps)); }
+// ---------------------------------------------------------------------- dk, dv
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapDO,
+           const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
+           const Params p) {
+    using C = Cfg<DP>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sK = smem_u32(smem), sV = sK + C::TILE;
+    const uint32_t sQ = sV + C::TILE, sDO = sQ + C::R0 * C::TILE;
+    float* rowdata = reinterpret_cast<float*>(smem + C::TILES);  // [2][lse, delta][128]
+    uint8_t* misc = smem + C::TILES + 2 * 2 * 512;
+    const uint32_t bars = smem_u32(misc);
+    const auto q_full = [&](int s) { return bars + 8u * s; };
+    const auto q_empty = [&](int s) { return bars + 8u * (3 + s); };
+    const auto do_full = [&](int s) { return bars + 8u * (6 + s); };
+    const auto do_empty = [&](int s) { return bars + 8u * (8 + s); };
+    const auto r_full = [&](int s) { return bars + 8u * (10 + s); };
+    const uint32_t kv_bar = bars + 96, s_bar = bars + 104, p_bar = bars + 112, dp_bar = bars + 120,
+                   ds_bar = bars + 128, done_bar = bars + 136;
+    const auto r_empty = [&](int s) { return bars + 144 + 8u * s; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 160);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* found = reinterpret_cast<int*>(tmem_slot + 2);
+    constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 256 + DP;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 10; ++i) mbar_init(bars + 8 * i, 1);
+        mbar_init(r_full(0), 32);
+        mbar_init(r_full(1), 32);
+        mbar_init(r_empty(0), kCompute / 32);
+        mbar_init(r_empty(1), kCompute / 32);
+        mbar_init(kv_bar, 1);
+        mbar_init(s_bar, 1);
+        mbar_init(p_bar, kCompute);
+        mbar_init(dp_bar, 1);
+        mbar_init(ds_bar, kCompute);
+        mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    pdl_trigger();
+    const int hk = blockIdx.y, tpt = p.tpt, G = p.a.Hq / p.a.Hkv;
+    if (warp == 0) {
+        int b = -1, item = 0, items = 0;
+        if ((sK & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
+        const bool skip = __any_sync(~0u, has_error(p.err));
+        if (skip || !find_tile(p.s, true, kRows, blockIdx.x, lane, b, item, items, p.err)) b = -1;
+        if (lane == 0) {
+            found[0] = b;
+            found[1] = item;  // the first keys of a sequence are seen most, and come first
+        }
+    }
+    if (warp == 1 && blockIdx.x == 0 && hk == 0) check_sequences(p.s, lane, p.err);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int b = found[0];
+    if (b >= 0) {
+        const int q0 = p.s.cu_q[b], nq = p.s.cu_q[b + 1] - q0;
+        const int k0 = p.s.cu_k[b], nk = p.s.cu_k[b + 1] - k0;
+        const int kv0 = found[1] * kRows;
+        // query tiles [i0, i0 + n)
+        const int i0 = (p.s.causal ? max(0, kv0 - (nk - nq)) : 0) / tpt;
+        const int n = max(0, (nq + tpt - 1) / tpt - i0);
+        const auto rows_of = [&](int i) { return G * min(tpt, nq - (i0 + i) * tpt); };
+
+        if (warp == 9) {
+            if (lane == 0 && n > 0) {
+                const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int h, int t) {
+                    for (int c = 0; c < C::PIECES; ++c)
+                        tma_load_3d(dst + c * kPiece, m, bar, 64 * c, h, t);
+                };
+                const uint32_t qbytes = C::PIECES * 128 * G * tpt;
+                mbar_arrive_expect_tx(kv_bar, 2 * C::TILE);
+                load(sK, &mapK, kv_bar, hk, k0 + kv0);
+                int iq = 0, id = 0;
+                for (int i = 0; i < n; ++i) {
+                    const int t = q0 + (i0 + i) * tpt;
+                    int s = i % C::R0;
+                    if (i >= C::R0 && !mbar_wait(q_empty(s), (i / C::R0 - 1) & 1, abort_flag, kWaitNs))
+                        break;
+                    mbar_arrive_expect_tx(q_full(s), qbytes);
+                    load(sQ + s * C::TILE, &mapQ, q_full(s), hk * G, t);
+                    ++iq;
+                    if (i == 0) load(sV, &mapV, kv_bar, hk, k0 + kv0);
+                    s = i % C::R1;
+                    if (i >= C::R1 && !mbar_wait(do_empty(s), (i / C::R1 - 1) & 1, abort_flag, kWaitNs))
+                        break;
+                    mbar_arrive_expect_tx(do_full(s), qbytes);
+                    load(sDO + s * C::TILE, &mapDO, do_full(s), hk * G, t);
+                    ++id;
+                }
+                // nothing is in flight when the CTA leaves
+                drain(kv_bar, 0);
+                for (int i = max(0, iq - C::R0); i < iq; ++i) drain(q_full(i % C::R0), (i / C::R0) & 1);
+                for (int i = max(0, id - C::R1); i < id; ++i) drain(do_full(i % C::R1), (i / C::R1) & 1);
+            }
+        } else if (warp == 10) {
+            // lse and delta of each query tile's rows; a row past the sequence or without
+            // a key has lse +inf (its weights are 0) and delta 0
+            for (int i = 0; i < n; ++i) {
+                if (i >= 2 && !warp_wait(r_empty(i & 1), (i / 2 - 1) & 1, abort_flag)) break;
+                const int rows = rows_of(i);
+                const long long at =
+                    (static_cast<long long>(hk) * p.s.Tq + q0 + (i0 + i) * tpt) * G;
+                float* dst = rowdata + (i & 1) * 256;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int r = u * 32 + lane;
+                    dst[r] = r < rows ? p.row_lse[at + r] : INFINITY;
+                    dst[128 + r] = r < rows ? p.row_delta[at + r] : 0.f;
+                }
+                mbar_arrive(r_full(i & 1));
+            }
+        } else if (warp == 8) {
+            const int ksteps = (p.a.D + 15) / 16;
+            const uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_g = idesc_bf16(128, 16 * ksteps, 0, 1);
+            // S^T_i, once its queries are there (rows past them zeroed: dK sums over them)
+            const auto scores = [&](int i) -> bool {
+                const int s = i % C::R0;
+                if (!warp_wait(q_full(s), (i / C::R0) & 1, abort_flag)) return false;
+                if (rows_of(i) < kRows) zero_tail(sQ + s * C::TILE, C::PIECES, rows_of(i), lane);
+                tc_fence_after();
+                if (lane == 0) {
+                    for (int k = 0; k < ksteps; ++k)
+                        mma_bf16(tmem + TM_S, desc_k(sK, k), desc_k(sQ + s * C::TILE, k), id_s, k > 0);
+                    mma_commit(s_bar);
+                }
+                __syncwarp();
+                return true;
+            };
+            bool ok = n == 0 || (warp_wait(kv_bar, 0, abort_flag) && scores(0));
+            for (int i = 0; i < n && ok; ++i) {
+                const int sd = i % C::R1, sq = i % C::R0;
+                ok = warp_wait(do_full(sd), (i / C::R1) & 1, abort_flag);
+                if (!ok) break;
+                if (rows_of(i) < kRows) zero_tail(sDO + sd * C::TILE, C::PIECES, rows_of(i), lane);
+                tc_fence_after();
+                if (lane == 0) {
+                    for (int k = 0; k < ksteps; ++k)
+                        mma_bf16(tmem + TM_DP, desc_k(sV, k), desc_k(sDO + sd * C::TILE, k), id_s,
+                                 k > 0);
+                    mma_commit(dp_bar);
+                }
+                __syncwarp();
+                ok = warp_wait(p_bar, i & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    for (int k = 0; k < kRows / 16; ++k)
+                        mma_bf16_ta(tmem + TM_DV, operand(tmem + TM_S, k),
+                                    desc_mn(sDO + sd * C::TILE, k), id_g, (i | k) != 0);
+                    mma_commit(do_empty(sd));
+                }
+                __syncwarp();
+                if (i + 1 < n) ok = scores(i + 1);
+                ok = ok && warp_wait(ds_bar, i & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    for (int k = 0; k < kRows / 16; ++k)
+                        mma_bf16_ta(tmem + TM_DK, operand(tmem + TM_DP, k),
+                                    desc_mn(sQ + sq * C::TILE, k), id_g, (i | k) != 0);
+                    mma_commit(q_empty(sq));
+                }
+                __syncwarp();
+            }
+            if (lane == 0) {
+                mma_commit(done_bar);
+                drain(done_bar, 0);
+            }
+            __syncwarp();
+        } else if (warp < 8) {
+            const int grp = warp >> 2, row = threadIdx.x & 127;
+            const int key = kv0 + row;  // in its sequence
+            const float c = p.scale * kLog2e;
+            const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+            bool ok = true;
+            for (int i = 0; i < n; ++i) {
+                const float* rd = rowdata + (i & 1) * 256 + 64 * grp;
+                // the first token of the tile that sees this key, as the first such column
+                const int from = p.s.causal ? (key - (nk - nq) - (i0 + i) * tpt) * G - 64 * grp : 0;
+                const bool diag = p.s.causal && kv0 + kRows - 1 - (nk - nq) > (i0 + i) * tpt;
+                ok = warp_wait(r_full(i & 1), (i >> 1) & 1, abort_flag) &&
+                     warp_wait(s_bar, i & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                float s[64], d[64];
+                load64(lanes + TM_S + 64 * grp, s);
+#pragma unroll
+                for (int q = 0; q < 64; q += 4) {
+                    const float4 e = *reinterpret_cast<const float4*>(rd + q);
+                    s[q] = exp2_fast(fmaf(s[q], c, -e.x));
+                    s[q + 1] = exp2_fast(fmaf(s[q + 1], c, -e.y));
+                    s[q + 2] = exp2_fast(fmaf(s[q + 2], c, -e.z));
+                    s[q + 3] = exp2_fast(fmaf(s[q + 3], c, -e.w));
+                }
+                if (diag) {
+#pragma unroll
+                    for (int q = 0; q < 64; ++q) s[q] = q >= from ? s[q] : 0.f;
+                }
+                store64(lanes + TM_S + 64 * grp, s);
+                tc_fence_before();
+                mbar_arrive(p_bar);
+                ok = warp_wait(dp_bar, i & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                load64(lanes + TM_DP + 64 * grp, d);
+#pragma unroll
+                for (int q = 0; q < 64; q += 4) {
+                    const float4 e = *reinterpret_cast<const float4*>(rd + 128 + q);
+                    d[q] = s[q] * (d[q] - e.x);
+                    d[q + 1] = s[q + 1] * (d[q + 1] - e.y);
+                    d[q + 2] = s[q + 2] * (d[q + 2] - e.z);
+                    d[q + 3] = s[q + 3] * (d[q + 3] - e.w);
+                }
+                if (diag) {
+#pragma unroll
+                    for (int q = 0; q < 64; ++q) d[q] = q >= from ? d[q] : 0.f;
+                }
+                store64(lanes + TM_DP + 64 * grp, d);
+                tc_fence_before();
+                mbar_arrive(ds_bar);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(r_empty(i & 1));
+            }
+            if (ok && n > 0) ok = mbar_wait(done_bar, 0, abort_flag, kWaitNs);
+            ok = __all_sync(~0u, ok);
+            if (ok) {
+                tc_fence_after();
+                const Heads& dst = grp == 0 ? p.dv : p.dk;
+                store_rows<DP>(lanes + (grp == 0 ? TM_DV : TM_DK), n > 0, grp == 0 ? 1.f : p.scale,
+                               smem + warp * 32 * DP * 2, lane, 0, p.a.D, [&](int r) -> bf16* {
+                                   const int k = kv0 + (warp & 3) * 32 + r;
+                                   return k < nk ? dst.row(k0 + k, hk) : nullptr;
+                               });
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (threadIdx.x == 0 && *abort_flag) raise_error(p.err, MOE_ERR_TIMEOUT);
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+template <int DP>
+cudaError_t backward(const Attention& p, cudaStream_t st) {
+    using C = Cfg<DP>;
+    const int G = p.a.Hq / p.a.Hkv, D = p.a.D, tpt = kRows / G;
+    float* second = p.delta + static_cast<size_t>(p.s.Tq) * p.a.Hq;
+    const Params prm{p.a, p.s, p.scale, p.out, p.dout, p.dq, p.dk, p.dv, p.lse, p.delta, second,
+                     p.err, tpt};
+    CUtensorMap mq, md, mk, mv;
+    if (p.s.Tq > 0 && (!make_tmap_heads(&mq, p.q, p.s.Tq, p.a.Hq, D, G, tpt) ||
+                       !make_tmap_heads(&md, p.dout, p.s.Tq, p.a.Hq, D, G, tpt)))
+        return cudaErrorInvalidValue;
+    if (p.s.Tk > 0 && (!make_tmap_heads(&mk, p.k, p.s.Tk, p.a.Hkv, D, 1, kRows) ||
+                       !make_tmap_heads(&mv, p.v, p.s.Tk, p.a.Hkv, D, 1, kRows)))
+        return cudaErrorInvalidValue;
+    // without queries or without keys no tile is loaded
+    if (p.s.Tq == 0) mq = md = mk;
+    if (p.s.Tk == 0) mk = mv = mq;
+    const long long qi = tile_bound(p.s.Tq, p.s.B, p.s.max_q, tpt);
+    if (p.s.Tq > 0 && qi > 0) {
+        auto kfn = dq_kernel<DP>;
+        cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             C::SMEM_Q);
+        if (e != cudaSuccess) return e;
+        LaunchScope ls("attention_dq", st);
+        e = launch_k(kfn, dim3(static_cast<unsigned>(qi), p.a.Hkv), dim3(kThreads), C::SMEM_Q, st,
+                     mq, md, mk, mv, prm);
+        if (e != cudaSuccess) return e;
+    }
+    const long long ki = tile_bound(p.s.Tk, p.s.B, p.s.max_k, kRows);
+    if (p.s.Tk == 0 || ki == 0) return cudaSuccess;
+    auto kfn = dkv_kernel<DP>;
+    const cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               C::SMEM_KV);
+    if (e != cudaSuccess) return e;
+    LaunchScope ls("attention_dkv", st);
+    return launch_k(kfn, dim3(static_cast<unsigned>(ki), p.a.Hkv), dim3(kThreads), C::SMEM_KV, st,
+                    mq, md, mk, mv, prm);
+}
 
 }  // namespace
 
 cudaError_t launch_attention_backward(const Attention& p, cudaStream_t st) {
-    if (p.s.Tq > 0) {
-        LaunchScope ls("attention_dq", st);
-        const cudaError_t e = launch_k(dq_kernel, row_grid(static_cast<long long>(p.s.Tq) * p.a.Hq),
-                                       dim3(kWarps * 32), 0, st, p);
-        if (e != cudaSuccess) return e;
-    }
-    if (p.s.Tk == 0) return cudaSuccess;
-    LaunchScope ls("attention_dkv", st);
-    return launch_k(dkv_kernel, row_grid(static_cast<long long>(p.s.Tk) * p.a.Hkv),
-                    dim3(kWarps * 32), 0, st, p);
+    return p.a.D <= 64 ? backward<64>(p, st) : backward<128>(p, st);
 }
 
 }  // namespace attn

@@ -87,7 +87,7 @@ struct Attention {
     float scale;
     Heads q, k, v, out, dout, dq, dk, dv;
     float* lse;
-    float* delta;  // backward scratch [Tq, Hq]
+    float* delta;  // backward scratch, 2 x [Hkv][Tq][G]
     int* err;
 };
 cudaError_t launch_attention_forward(const Attention& p, cudaStream_t st);

@@ -279,7 +279,7 @@ int moe_attention_forward(moe_attn_shape a, moe_packed s, float scale, moe_heads
 
 size_t moe_attention_backward_workspace_size(moe_attn_shape a, moe_packed s) {
     if (check_attn(a) || check_tokens(s.Tq)) return 0;
-    return sizeof(float) * static_cast<size_t>(s.Tq) * a.Hq;
+    return 2 * sizeof(float) * static_cast<size_t>(s.Tq) * a.Hq;
 }
 
 int moe_attention_backward(moe_attn_shape a, moe_packed s, float scale, moe_heads dout,
