@@ -24,8 +24,8 @@
  *   - What only the device can see (offsets that do not ascend or pass the
  *     arrays, a sequence longer than the stated bound, a position outside the
  *     rotary table, a slot or page outside the cache) sets MOE_ERR_BAD_INDEX in
- *     the status word; the row or sequence concerned is left out. Nothing is read
- *     or written out of bounds.
+ *     the status word; results of the row or sequence concerned are undefined.
+ *     Nothing is read or written out of bounds.
  *   - Sums, softmax statistics and norms are fp32; results are rounded once to
  *     bf16. Where a product runs on the tensor cores, the softmax weights and
  *     their gradients are its bf16 operands. Every result is the same from run to
