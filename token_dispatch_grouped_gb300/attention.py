@@ -61,7 +61,8 @@ class Attention:
 
     eps: of the RMS norm of the heads. rope_table: from rope_table() (None: no
     rotation); rope_layout "half" or "interleaved". scale: of the scores, by
-    default D^-1/2. The workspace is kept and grows to the largest call."""
+    default D^-1/2. Calls run on the current stream. The workspace is kept, grows to the
+    largest call and is shared by all of them: use one Attention per stream."""
 
     def __init__(self, Hq: int, Hkv: int, D: int, device="cuda", eps: float = 1e-6,
                  rope_table: torch.Tensor | None = None, rope_layout: str = "half",
@@ -83,23 +84,25 @@ class Attention:
         self._ws = None
 
     # ---------------------------------------------------------------- checks
-    def _heads(self, t, T: int, H: int, where: str):
-        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != T or t.shape[1] != H or \
-                t.shape[2] != self.D or (t.stride(2) != 1 and self.D > 1 and T > 0) or \
-                not t.is_cuda:
+    def _heads(self, t, T: int, H: int, where: str) -> B.MoeHeads:
+        """The view of t, a bf16 tensor [T, H, D] with dense values on the device."""
+        if t.dtype is not torch.bfloat16 or t.shape != (T, H, self.D) or not t.is_cuda:
             raise B.MoeError(B.MOE_ERR_INVALID_ARG, where)
-        return t
-
-    def _ints(self, t, n: int, where: str, dtype=torch.int32):
-        if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        ts, hs, vs = t.stride()
+        if vs != 1 and T > 0:
             raise B.MoeError(B.MOE_ERR_INVALID_ARG, where)
-        return t
+        return B.MoeHeads(t.data_ptr(), ts, hs)
 
-    def _norm(self, wq, wk, where: str):
-        for w in (wq, wk):
-            if w is not None and (w.dtype != torch.float32 or w.numel() != self.D or
-                                  not w.is_contiguous() or not w.is_cuda):
-                raise B.MoeError(B.MOE_ERR_INVALID_ARG, where)
+    def _ints(self, t, n: int, where: str, dtype=torch.int32) -> int:
+        if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+            raise B.MoeError(B.MOE_ERR_INVALID_ARG, where)
+        return t.data_ptr()
+
+    def _norm(self, w, where: str) -> int | None:
+        return None if w is None else self._ints(w, self.D, where, torch.float32)
+
+    def _positions(self, positions, T: int, where: str) -> int | None:
+        return None if self.table is None else self._ints(positions, T, where)
 
     def _out(self, T: int, H: int) -> torch.Tensor:
         return torch.empty(T, H, self.D, dtype=torch.bfloat16, device=self.device)
@@ -115,132 +118,137 @@ class Attention:
     def norm_rope(self, q, k, wq, wk, positions, q_out=None, k_out=None):
         """Normed (unless wq is None) and rotated (unless without a table) heads."""
         T, where = q.shape[0], "norm_rope"
-        self._heads(q, T, self.Hq, where)
-        self._heads(k, T, self.Hkv, where)
-        self._norm(wq, wk, where)
-        if self.table is not None:
-            self._ints(positions, T, where)
-        q_out = self._out(T, self.Hq) if q_out is None else self._heads(q_out, T, self.Hq, where)
-        k_out = self._out(T, self.Hkv) if k_out is None else self._heads(k_out, T, self.Hkv, where)
-        B.moe_norm_rope(self.a, T, q, k, wq, wk, self.eps, positions, self.rope, q_out, k_out)
+        if q_out is None:
+            q_out = self._out(T, self.Hq)
+        if k_out is None:
+            k_out = self._out(T, self.Hkv)
+        B.moe_norm_rope(self.a, T, self._heads(q, T, self.Hq, where),
+                        self._heads(k, T, self.Hkv, where), self._norm(wq, where),
+                        self._norm(wk, where), self.eps, self._positions(positions, T, where),
+                        self.rope, self._heads(q_out, T, self.Hq, where),
+                        self._heads(k_out, T, self.Hkv, where))
         return q_out, k_out
 
     def norm_rope_backward(self, dq_out, dk_out, q, k, wq, wk, positions, dq=None, dk=None):
         """dq, dk, dwq, dwk (the last two None without a norm)."""
         T, where = q.shape[0], "norm_rope_backward"
-        for x in (dq_out, q):
-            self._heads(x, T, self.Hq, where)
-        for x in (dk_out, k):
-            self._heads(x, T, self.Hkv, where)
-        self._norm(wq, wk, where)
-        if self.table is not None:
-            self._ints(positions, T, where)
-        dq = self._out(T, self.Hq) if dq is None else self._heads(dq, T, self.Hq, where)
-        dk = self._out(T, self.Hkv) if dk is None else self._heads(dk, T, self.Hkv, where)
+        Hq, Hkv = self.Hq, self.Hkv
+        if dq is None:
+            dq = self._out(T, Hq)
+        if dk is None:
+            dk = self._out(T, Hkv)
         dwq = dwk = ws = None
         if wq is not None:
-            dw = torch.empty(2, self.D, dtype=torch.float32, device=self.device)
-            dwq, dwk = dw[0], dw[1]
+            dwq = torch.empty(self.D, dtype=torch.float32, device=self.device)
+            dwk = torch.empty(self.D, dtype=torch.float32, device=self.device)
             ws = self._workspace(B.moe_norm_rope_workspace_size(self.a, T))
-        B.moe_norm_rope_backward(self.a, T, dq_out, dk_out, q, k, wq, wk, self.eps, positions,
-                                 self.rope, dq, dk, dwq, dwk, ws)
+        B.moe_norm_rope_backward(self.a, T, self._heads(dq_out, T, Hq, where),
+                                 self._heads(dk_out, T, Hkv, where),
+                                 self._heads(q, T, Hq, where), self._heads(k, T, Hkv, where),
+                                 self._norm(wq, where), self._norm(wk, where), self.eps,
+                                 self._positions(positions, T, where), self.rope,
+                                 self._heads(dq, T, Hq, where), self._heads(dk, T, Hkv, where),
+                                 dwq, dwk, ws)
         return dq, dk, dwq, dwk
 
     # ------------------------------------------------------------ packed batches
-    def _packed(self, q, k, cu_q, max_q, cu_k, max_k, causal, where):
-        self._ints(cu_q, cu_q.numel(), where)
-        self._ints(cu_k, cu_q.numel(), where)
-        return B.MoePacked(cu_q.numel() - 1, q.shape[0], k.shape[0], max_q, max_k, int(causal),
-                           cu_q.data_ptr(), cu_k.data_ptr())
+    def _packed(self, Tq, Tk, cu_q, max_q, cu_k, max_k, causal, where):
+        n = cu_q.numel()
+        q = self._ints(cu_q, n, where)
+        k = q if cu_k is None else self._ints(cu_k, n, where)
+        return B.MoePacked(n - 1, Tq, Tk, max_q, max_q if cu_k is None else max_k, bool(causal), q,
+                           k)
 
     def forward(self, q, k, v, cu_q, max_q, cu_k=None, max_k=None, causal=True, out=None,
                 lse=None):
         """out [Tq, Hq, D] and lse [Tq, Hq] of the sequences between the offsets cu_q
         and cu_k (int32, on the device; cu_k = None: those of the queries). max_q and
         max_k bound their lengths."""
-        where = "attention_forward"
-        cu_k, max_k = (cu_q, max_q) if cu_k is None else (cu_k, max_k)
-        Tq, Tk = q.shape[0], k.shape[0]
-        self._heads(q, Tq, self.Hq, where)
-        self._heads(k, Tk, self.Hkv, where)
-        self._heads(v, Tk, self.Hkv, where)
-        out = self._out(Tq, self.Hq) if out is None else self._heads(out, Tq, self.Hq, where)
+        Tq, Tk, Hq, Hkv, where = q.shape[0], k.shape[0], self.Hq, self.Hkv, "attention_forward"
+        if out is None:
+            out = self._out(Tq, Hq)
         if lse is None:
-            lse = torch.empty(Tq, self.Hq, dtype=torch.float32, device=self.device)
-        else:
-            self._ints(lse, Tq * self.Hq, where, torch.float32)
-        s = self._packed(q, k, cu_q, max_q, cu_k, max_k, causal, where)
-        B.moe_attention_forward(self.a, s, self.scale, q, k, v, out, lse)
+            lse = torch.empty(Tq, Hq, dtype=torch.float32, device=self.device)
+        B.moe_attention_forward(self.a,
+                                self._packed(Tq, Tk, cu_q, max_q, cu_k, max_k, causal, where),
+                                self.scale, self._heads(q, Tq, Hq, where),
+                                self._heads(k, Tk, Hkv, where), self._heads(v, Tk, Hkv, where),
+                                self._heads(out, Tq, Hq, where),
+                                self._ints(lse, Tq * Hq, where, torch.float32))
         return out, lse
 
     def backward(self, dout, q, k, v, out, lse, cu_q, max_q, cu_k=None, max_k=None, causal=True,
                  dq=None, dk=None, dv=None):
         """dq, dk, dv of forward()."""
-        where = "attention_backward"
-        cu_k, max_k = (cu_q, max_q) if cu_k is None else (cu_k, max_k)
-        Tq, Tk = q.shape[0], k.shape[0]
-        for x in (dout, q, out):
-            self._heads(x, Tq, self.Hq, where)
-        for x in (k, v):
-            self._heads(x, Tk, self.Hkv, where)
-        self._ints(lse, Tq * self.Hq, where, torch.float32)
-        dq = self._out(Tq, self.Hq) if dq is None else self._heads(dq, Tq, self.Hq, where)
-        dk = self._out(Tk, self.Hkv) if dk is None else self._heads(dk, Tk, self.Hkv, where)
-        dv = self._out(Tk, self.Hkv) if dv is None else self._heads(dv, Tk, self.Hkv, where)
-        s = self._packed(q, k, cu_q, max_q, cu_k, max_k, causal, where)
-        ws = self._workspace(B.moe_attention_backward_workspace_size(self.a, s))
-        B.moe_attention_backward(self.a, s, self.scale, dout, q, k, v, out, lse, dq, dk, dv, ws)
+        Tq, Tk, Hq, Hkv, where = q.shape[0], k.shape[0], self.Hq, self.Hkv, "attention_backward"
+        if dq is None:
+            dq = self._out(Tq, Hq)
+        if dk is None:
+            dk = self._out(Tk, Hkv)
+        if dv is None:
+            dv = self._out(Tk, Hkv)
+        s = self._packed(Tq, Tk, cu_q, max_q, cu_k, max_k, causal, where)
+        B.moe_attention_backward(self.a, s, self.scale, self._heads(dout, Tq, Hq, where),
+                                 self._heads(q, Tq, Hq, where), self._heads(k, Tk, Hkv, where),
+                                 self._heads(v, Tk, Hkv, where), self._heads(out, Tq, Hq, where),
+                                 self._ints(lse, Tq * Hq, where, torch.float32),
+                                 self._heads(dq, Tq, Hq, where), self._heads(dk, Tk, Hkv, where),
+                                 self._heads(dv, Tk, Hkv, where),
+                                 self._workspace(
+                                     B.moe_attention_backward_workspace_size(self.a, s)))
         return dq, dk, dv
 
     # --------------------------------------------------------------- paged cache
     def _cache(self, k_pages, v_pages, where):
+        shape = k_pages.shape
         for x in (k_pages, v_pages):
-            if x.dtype != torch.bfloat16 or x.dim() != 4 or x.shape != k_pages.shape or \
-                    x.shape[1] != self.Hkv or x.shape[3] != self.D or not x.is_contiguous() or \
-                    not x.is_cuda:
+            if x.dtype is not torch.bfloat16 or x.dim() != 4 or x.shape != shape or \
+                    not x.is_contiguous() or not x.is_cuda:
                 raise B.MoeError(B.MOE_ERR_INVALID_ARG, where)
-        return B.MoeKvCache(k_pages.data_ptr(), v_pages.data_ptr(), k_pages.shape[0],
-                            k_pages.shape[2])
+        pages, heads, size, values = shape
+        if heads != self.Hkv or values != self.D:
+            raise B.MoeError(B.MOE_ERR_INVALID_ARG, where)
+        return B.MoeKvCache(k_pages.data_ptr(), v_pages.data_ptr(), pages, size)
 
     def append(self, q, k, v, wq, wk, positions, slots, k_pages, v_pages, q_out=None):
         """norm_rope of new tokens; keys and values go to slots (int64) of the pages
         [pages, Hkv, page_size, D], the queries are returned."""
         T, where = q.shape[0], "append"
-        self._heads(q, T, self.Hq, where)
-        self._heads(k, T, self.Hkv, where)
-        self._heads(v, T, self.Hkv, where)
-        self._norm(wq, wk, where)
-        if self.table is not None:
-            self._ints(positions, T, where)
-        self._ints(slots, T, where, torch.int64)
-        cache = self._cache(k_pages, v_pages, where)
-        q_out = self._out(T, self.Hq) if q_out is None else self._heads(q_out, T, self.Hq, where)
-        B.moe_kv_append(self.a, T, q, k, v, wq, wk, self.eps, positions, self.rope, slots, q_out,
-                        cache)
+        if q_out is None:
+            q_out = self._out(T, self.Hq)
+        B.moe_kv_append(self.a, T, self._heads(q, T, self.Hq, where),
+                        self._heads(k, T, self.Hkv, where), self._heads(v, T, self.Hkv, where),
+                        self._norm(wq, where), self._norm(wk, where), self.eps,
+                        self._positions(positions, T, where), self.rope,
+                        self._ints(slots, T, where, torch.int64),
+                        self._heads(q_out, T, self.Hq, where),
+                        self._cache(k_pages, v_pages, where))
         return q_out
 
     def decode(self, q, k_pages, v_pages, block_table, kv_lens, max_kv, out=None):
         """Attention of the newest q.shape[0] / B tokens of B sequences, whose cached
-        lengths (those tokens included) are kv_lens, at most max_kv."""
+        lengths (those tokens included) are kv_lens, at most max_kv. block_table
+        [B, pages of a sequence] int32."""
         T, nb, where = q.shape[0], kv_lens.numel(), "decode"
-        self._heads(q, T, self.Hq, where)
-        self._ints(kv_lens, nb, where)
+        if out is None:
+            out = self._out(T, self.Hq)
         if T == 0 and nb == 0:
-            return self._out(0, self.Hq) if out is None else out
-        if nb == 0 or T % nb or T < nb or block_table.dtype != torch.int32 or \
-                block_table.dim() != 2 or block_table.shape[0] != nb or \
-                block_table.stride(1) != 1 or not block_table.is_cuda or \
-                (nb > 1 and block_table.stride(0) < block_table.shape[1]):
+            return out
+        if nb == 0 or T % nb or T < nb or block_table.dtype is not torch.int32 or \
+                block_table.dim() != 2 or not block_table.is_cuda:
             raise B.MoeError(B.MOE_ERR_INVALID_ARG, where)
+        rows, wide = block_table.shape
+        stride = block_table.stride()
         cache = self._cache(k_pages, v_pages, where)
-        if max_kv > block_table.shape[1] * k_pages.shape[2]:
+        if rows != nb or (wide > 1 and stride[1] != 1) or (nb > 1 and stride[0] < wide) or \
+                max_kv > wide * cache.page_size:
             raise B.MoeError(B.MOE_ERR_INVALID_ARG, where)
-        out = self._out(T, self.Hq) if out is None else self._heads(out, T, self.Hq, where)
         n = T // nb
         ws = self._workspace(B.moe_attention_decode_workspace_size(self.a, nb, n, max_kv))
-        stride = block_table.stride(0) if nb > 1 else block_table.shape[1]
-        B.moe_attention_decode(self.a, nb, n, max_kv, self.scale, q, cache, block_table, stride,
-                               kv_lens, out, ws)
+        B.moe_attention_decode(self.a, nb, n, max_kv, self.scale,
+                               self._heads(q, T, self.Hq, where), cache, block_table.data_ptr(),
+                               stride[0] if nb > 1 else wide, self._ints(kv_lens, nb, where),
+                               self._heads(out, T, self.Hq, where), ws)
         return out
 
     def check_error(self) -> None:
