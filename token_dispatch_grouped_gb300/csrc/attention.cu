@@ -141,7 +141,7 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
                 for (; i < 2 * n; ++i) {  // K and V tiles in turn
                     const int slot = i % C::STAGES;
                     if (i >= C::STAGES &&
-                        !mbar_wait(empty(slot), (i / C::STAGES - 1) & 1, abort_flag, kWaitNs))
+                        !wait_phase(empty(slot), (i / C::STAGES - 1) & 1, abort_flag))
                         break;
                     mbar_arrive_expect_tx(full(slot), C::TILE);
                     for (int c = 0; c < C::PIECES; ++c)
@@ -156,15 +156,14 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
             }
         } else if (warp == 8) {
             // ----------------------------------------------------- tensor cores
-            const int ksteps = (p.a.D + 15) / 16;
-            const uint32_t id_s = idesc_bf16(128, 128, 0, 0);
-            const uint32_t id_o = idesc_bf16(128, 16 * ksteps, 0, 1);
+            constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, DP, 0, 1);
             const auto scores = [&](int x, int slot) {
-                if (lane == 0) {
-                    for (int k = 0; k < ksteps; ++k)
-                        mma_bf16(tmem + C::TM_S + 128 * x, desc_k(sQ + x * C::TILE, k),
-                                 desc_k(sKV + slot * C::TILE, k), id_s, k > 0);
-                    mma_commit(s_bar(x));
+                const uint64_t ad = desc_d(sQ + x * C::TILE), bd = desc_d(sKV + slot * C::TILE);
+                const uint32_t dst = tmem + C::TM_S + 128 * x, bar = s_bar(x);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k) mma_bf16(dst, ad + kd(k), bd + kd(k), id_s, k > 0);
+                    mma_commit(bar);
                 }
                 __syncwarp();
             };
@@ -175,7 +174,8 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
                     ok = warp_wait(q_bar(x), 0, abort_flag);
                     if (ok) scores(x, 0);
                 }
-            if (ok && n > 0 && lane == 0) mma_commit(empty(0));
+            if (ok && n > 0 && elect_one()) mma_commit(empty(0));
+            __syncwarp();
             for (int j = 0; j < n && ok; ++j) {
                 const int iv = 2 * j + 1, ik = 2 * j + 2;
                 const int sv = iv % C::STAGES, sk = ik % C::STAGES;
@@ -189,26 +189,31 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
                     ok = warp_wait(p_bar(x), j & 1, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    if (lane == 0) {
+                    const uint64_t vd = desc_r(sKV + sv * C::TILE);
+                    const uint32_t dst = tmem + C::TM_O + DP * x, src = tmem + C::TM_S + 128 * x;
+                    const uint32_t add = j > 0, bar = o_bar(x);
+                    const bool last = j + 1 == tiles[x];
+                    if (elect_one()) {
+#pragma unroll
                         for (int k = 0; k < kRows / 16; ++k)
-                            mma_bf16_ta(tmem + C::TM_O + DP * x, tmem + C::TM_S + 128 * x + 8 * k,
-                                        desc_mn(sKV + sv * C::TILE, k), id_o, (j | k) != 0);
-                        if (j + 1 == tiles[x]) mma_commit(o_bar(x));
+                            mma_bf16_ta(dst, src + 8 * k, vd + kr(k), id_o, k > 0 ? 1u : add);
+                        if (last) mma_commit(bar);
                     }
                     __syncwarp();
                     if (j + 1 < tiles[x]) scores(x, sk);
                 }
                 if (!ok) break;
-                if (lane == 0) {
-                    mma_commit(empty(sv));
-                    if (j + 1 < n) mma_commit(empty(sk));
+                const uint32_t ev = empty(sv), ek = empty(sk);
+                const bool more = j + 1 < n;
+                if (elect_one()) {
+                    mma_commit(ev);
+                    if (more) mma_commit(ek);
                 }
                 __syncwarp();
             }
-            if (lane == 0) {
-                mma_commit(done_bar);
-                drain(done_bar, 0);
-            }
+            if (elect_one()) mma_commit(done_bar);
+            __syncwarp();
+            drain(done_bar, 0);
             __syncwarp();
         } else {
             // ---------------------------------------------------------- softmax

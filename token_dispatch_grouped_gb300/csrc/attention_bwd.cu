@@ -13,10 +13,11 @@
 //               keys are rows: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.
 //               The G heads of a group are rows of the same tiles, so their sum is the
 //               product's.
-// Roles as in the forward: a TMA warp, a warp that issues the tcgen05 products, and two
-// groups of four warps that turn scores into weights, each for 64 of the 128 columns of
-// every row; P and dS go back to TMEM as bf16 operands over the columns that their group
-// has read. The order of the products (dP, [P] dV, next S, [dS] dK) leaves the tensor
+// Roles as in the forward: a TMA warp, a warp that issues the tcgen05 products, and four
+// groups of four warps that turn scores into weights, each for 32 of the 128 columns of
+// every row (with two groups of 64 columns the tensor cores waited for them: 1.67 and 1.94
+// million cycles a SM for dq and dkv of 8192 tokens, 32/8 heads of 128, against XXX);
+// P and dS go back to TMEM as bf16 operands over the columns that their group has read. The order of the products (dP, [P] dV, next S, [dS] dK) leaves the tensor
 // cores work while the other warps compute: P while dP runs, dS while dV and the next S
 // run. TMEM: dq_kernel S twice, dP, dQ; dkv_kernel S, dP, dV, dK (4 x 128 columns).
 //
@@ -29,8 +30,8 @@ namespace moe {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 384;   // 8 compute warps, tensor cores, TMA, row data, (idle)
-constexpr int kCompute = 256;
+constexpr int kCompute = 16;  // warps: four groups of four, 32 columns of every row each
+constexpr int kThreads = (kCompute + 3) * 32;  // and tensor cores, TMA, row data
 constexpr float kLog2e = 1.44269504088896341f;
 
 struct Params {
@@ -50,63 +51,26 @@ struct Cfg {
     static constexpr int TILE = PIECES * kPiece;
     static constexpr int R0 = 3, R1 = 2;  // ring stages: the operand used twice, the other
     static constexpr int TILES = (2 + R0 + R1) * TILE;
-    static constexpr int SMEM_Q = TILES + 2 * 512 + 256;       // delta halves, barriers
+    static constexpr int SMEM_Q = TILES + 4 * 512 + 256;       // parts of delta, barriers
     static constexpr int SMEM_KV = TILES + 2 * 2 * 512 + 256;  // two slots of lse and delta
 };
 
-// 64 columns of TMEM as fp32.
-__device__ __forceinline__ void load64(uint32_t t, float (&v)[64]) {
+// 32 columns of TMEM as fp32.
+__device__ __forceinline__ void load32(uint32_t t, float (&v)[32]) {
     tmem_ld32(t, *reinterpret_cast<uint32_t(*)[32]>(v));
-    tmem_ld32(t + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
     tmem_ld_wait();
 }
-// 64 fp32 values as 32 columns of bf16 pairs.
-__device__ __forceinline__ void store64(uint32_t t, const float (&v)[64]) {
-    uint32_t w[32];
+// 32 fp32 values as 16 columns of bf16 pairs.
+__device__ __forceinline__ void store32(uint32_t t, const float (&v)[32]) {
+    uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1]);
-    tmem_st32(t, w);
+    for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1]);
+    tmem_st16(t, w);
     tmem_st_wait();
 }
-// k-th 16 columns of a bf16 operand that the two groups wrote: group 0's 64 columns at
-// t, group 1's at t + 64 (over the scores that each of them read).
-__device__ __forceinline__ uint32_t operand(uint32_t t, int k) {
-    return t + (k < 4 ? 8 * k : 64 + 8 * (k - 4));
-}
-
-// 32 rows x W columns (fp32, TMEM columns t ..) of one warp, times f, as bf16 rows:
-// row(r) gives the row's destination or nullptr. stg: 32 x W x 2 bytes of shared memory.
-template <int W, class Row>
-__device__ __forceinline__ void store_rows(uint32_t t, bool any, float f, uint8_t* stg, int lane,
-                                           int col0, int D, Row row) {
-    constexpr int CH = W / 8;
-#pragma unroll
-    for (int q = 0; q < W; q += 32) {
-        uint32_t o[32];
-        if (any) {
-            tmem_ld32(t + q, o);
-            tmem_ld_wait();
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = any ? __uint_as_float(o[8 * i + e]) * f : 0.f;
-            *reinterpret_cast<uint4*>(stg + lane * W * 2 + ((q / 8 + i) ^ (lane & (CH - 1))) * 16) =
-                pack8(v);
-        }
-    }
-    __syncwarp();
-    constexpr int RPI = 32 / CH;
-#pragma unroll 4
-    for (int i = 0; i < 32; i += RPI) {
-        const int rl = i + lane / CH, ch = lane % CH;
-        bf16* dst = row(rl);
-        if (dst != nullptr && col0 + ch * 8 < D)
-            *reinterpret_cast<uint4*>(dst + col0 + ch * 8) =
-                *reinterpret_cast<const uint4*>(stg + rl * W * 2 + (ch ^ (rl & (CH - 1))) * 16);
-    }
-}
+// k-th 16 columns of a bf16 operand that the groups wrote: group g's 32 columns in the
+// 16 TMEM columns at t + 32 g, over scores that it has read itself.
+__device__ __forceinline__ uint32_t operand(uint32_t t, int k) { return t + 32 * (k >> 1) + 8 * (k & 1); }
 
 // ---------------------------------------------------------------------- dq
 template <int DP>
@@ -118,8 +82,8 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sQ = smem_u32(smem), sDO = sQ + C::TILE;
     const uint32_t sK = sDO + C::TILE, sV = sK + C::R0 * C::TILE;
-    float* half_delta = reinterpret_cast<float*>(smem + C::TILES);  // [2][128]
-    uint8_t* misc = smem + C::TILES + 1024;
+    float* part_delta = reinterpret_cast<float*>(smem + C::TILES);  // [4][128]
+    uint8_t* misc = smem + C::TILES + 4 * 512;
     const uint32_t bars = smem_u32(misc);
     const auto k_full = [&](int s) { return bars + 8u * s; };
     const auto k_empty = [&](int s) { return bars + 8u * (3 + s); };
@@ -144,24 +108,24 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 8) {
+    if (warp == kCompute) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
     pdl_wait();
     pdl_trigger();
-    const int hk = blockIdx.y, tpt = p.tpt, G = p.a.Hq / p.a.Hkv;
+    const int hk = blockIdx.x % p.a.Hkv, tpt = p.tpt, G = p.a.Hq / p.a.Hkv;
     if (warp == 0) {
         int b = -1, item = 0, items = 0;
         if ((sQ & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
         const bool skip = __any_sync(~0u, has_error(p.err));
-        if (skip || !find_tile(p.s, false, tpt, blockIdx.x, lane, b, item, items, p.err)) b = -1;
+        if (skip || !find_tile(p.s, false, tpt, blockIdx.x / p.a.Hkv, lane, b, item, items, p.err)) b = -1;
         if (lane == 0) {
             found[0] = b;
             found[1] = items - 1 - item;  // the longest rows of a sequence first
         }
     }
-    if (warp == 1 && blockIdx.x == 0 && hk == 0) check_sequences(p.s, lane, p.err);
+    if (warp == 1 && blockIdx.x == 0) check_sequences(p.s, lane, p.err);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -174,7 +138,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
         const int seen = p.s.causal ? max(0, min(nk, min(first + tpt, nq) + nk - nq)) : nk;
         const int n = (seen + kRows - 1) / kRows;
 
-        if (warp == 9) {
+        if (warp == kCompute + 1) {
             if (lane == 0 && n > 0) {
                 const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int h, int t) {
                     for (int c = 0; c < C::PIECES; ++c)
@@ -186,7 +150,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                 int jk = 0, jv = 0;
                 for (int j = 0; j < n; ++j) {
                     int s = j % C::R0;
-                    if (j >= C::R0 && !mbar_wait(k_empty(s), (j / C::R0 - 1) & 1, abort_flag, kWaitNs))
+                    if (j >= C::R0 && !wait_phase(k_empty(s), (j / C::R0 - 1) & 1, abort_flag))
                         break;
                     mbar_arrive_expect_tx(k_full(s), C::TILE);
                     load(sK + s * C::TILE, &mapK, k_full(s), hk, k0 + j * kRows);
@@ -196,7 +160,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                         load(sDO, &mapDO, do_bar, hk * G, q0 + first);
                     }
                     s = j % C::R1;
-                    if (j >= C::R1 && !mbar_wait(v_empty(s), (j / C::R1 - 1) & 1, abort_flag, kWaitNs))
+                    if (j >= C::R1 && !wait_phase(v_empty(s), (j / C::R1 - 1) & 1, abort_flag))
                         break;
                     mbar_arrive_expect_tx(v_full(s), C::TILE);
                     load(sV + s * C::TILE, &mapV, v_full(s), hk, k0 + j * kRows);
@@ -208,9 +172,8 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                 for (int j = max(0, jk - C::R0); j < jk; ++j) drain(k_full(j % C::R0), (j / C::R0) & 1);
                 for (int j = max(0, jv - C::R1); j < jv; ++j) drain(v_full(j % C::R1), (j / C::R1) & 1);
             }
-        } else if (warp == 8) {
-            const int ksteps = (p.a.D + 15) / 16;
-            const uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_q = idesc_bf16(128, 16 * ksteps, 0, 1);
+        } else if (warp == kCompute) {
+            constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_q = idesc_bf16(128, DP, 0, 1);
             // S_j, once its keys are there
             const auto scores = [&](int j) -> bool {
                 const int s = j % C::R0;
@@ -218,11 +181,12 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                 if (seen - j * kRows < kRows)
                     zero_tail(sK + s * C::TILE, C::PIECES, seen - j * kRows, lane);
                 tc_fence_after();
-                if (lane == 0) {
-                    for (int k = 0; k < ksteps; ++k)
-                        mma_bf16(tmem + TM_S + 128 * (j & 1), desc_k(sQ, k),
-                                 desc_k(sK + s * C::TILE, k), id_s, k > 0);
-                    mma_commit(s_bar(j & 1));
+                const uint64_t ad = desc_d(sQ), bd = desc_d(sK + s * C::TILE);
+                const uint32_t dst = tmem + TM_S + 128 * (j & 1), bar = s_bar(j & 1);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k) mma_bf16(dst, ad + kd(k), bd + kd(k), id_s, k > 0);
+                    mma_commit(bar);
                 }
                 __syncwarp();
                 return true;
@@ -234,32 +198,36 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                 ok = warp_wait(v_full(sv), (j / C::R1) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    for (int k = 0; k < ksteps; ++k)
-                        mma_bf16(tmem + TM_DP, desc_k(sDO, k), desc_k(sV + sv * C::TILE, k), id_s,
-                                 k > 0);
+                const uint64_t dod = desc_d(sDO), vd = desc_d(sV + sv * C::TILE);
+                const uint32_t ve = v_empty(sv);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k)
+                        mma_bf16(tmem + TM_DP, dod + kd(k), vd + kd(k), id_s, k > 0);
                     mma_commit(dp_bar);
-                    mma_commit(v_empty(sv));
+                    mma_commit(ve);
                 }
                 __syncwarp();
                 if (j + 1 < n) ok = scores(j + 1);
                 ok = ok && warp_wait(ds_bar, j & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
+                const uint64_t kdesc = desc_r(sK + sk * C::TILE);
+                const uint32_t ke = k_empty(sk), add = j > 0;
+                if (elect_one()) {
+#pragma unroll
                     for (int k = 0; k < kRows / 16; ++k)
-                        mma_bf16_ta(tmem + TM_DQ, operand(tmem + TM_DP, k),
-                                    desc_mn(sK + sk * C::TILE, k), id_q, (j | k) != 0);
-                    mma_commit(k_empty(sk));
+                        mma_bf16_ta(tmem + TM_DQ, operand(tmem + TM_DP, k), kdesc + kr(k), id_q,
+                                    k > 0 ? 1u : add);
+                    mma_commit(ke);
                 }
                 __syncwarp();
             }
-            if (lane == 0) {
-                mma_commit(done_bar);
-                drain(done_bar, 0);
-            }
+            if (elect_one()) mma_commit(done_bar);
             __syncwarp();
-        } else if (warp < 8) {
+            drain(done_bar, 0);
+            __syncwarp();
+        } else if (warp < kCompute) {
             const int grp = warp >> 2, row = threadIdx.x & 127;
             const int token = first + row / G, g = row % G;
             const bool valid = row < G * tpt && token < nq;
@@ -267,14 +235,14 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
             const int open = p.s.causal ? first + 1 + nk - nq : nk;  // keys that every row sees
             const float c = p.scale * kLog2e;
             const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-            // delta: each group sums half of the row's columns
+            // delta: each group sums a quarter of the row's columns
             float delta = 0.f, lse2 = INFINITY;
             if (valid) {
                 const bf16* o = p.out.row(q0 + token, hk * G + g);
                 const bf16* d = p.dout.row(q0 + token, hk * G + g);
 #pragma unroll
-                for (int i = 0; i < DP / 16; ++i) {
-                    const int col = grp * (DP / 2) + i * 8;
+                for (int i = 0; i < DP / 32; ++i) {
+                    const int col = grp * (DP / 4) + i * 8;
                     if (col >= p.a.D) break;
                     float x[8], y[8];
                     unpack8(*reinterpret_cast<const uint4*>(o + col), x);
@@ -285,9 +253,10 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                 const float e = p.lse[static_cast<long long>(q0 + token) * p.a.Hq + hk * G + g];
                 lse2 = e == -INFINITY ? INFINITY : e * kLog2e;
             }
-            half_delta[grp * 128 + row] = delta;
-            asm volatile("bar.sync 1, %0;" ::"n"(kCompute) : "memory");
-            delta = half_delta[row] + half_delta[128 + row];
+            part_delta[grp * 128 + row] = delta;
+            bar_sync(1, kCompute * 32);
+            delta = (part_delta[row] + part_delta[128 + row]) +
+                    (part_delta[256 + row] + part_delta[384 + row]);
             if (valid && grp == 0) {
                 const long long at = (static_cast<long long>(hk) * p.s.Tq + q0 + token) * G + g;
                 p.row_lse[at] = lse2;
@@ -298,10 +267,10 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                 ok = warp_wait(s_bar(j & 1), (j >> 1) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                float s[64], d[64];
-                load64(lanes + TM_S + 128 * (j & 1) + 64 * grp, s);
+                float s[32], d[32];
+                load32(lanes + TM_S + 128 * (j & 1) + 32 * grp, s);
 #pragma unroll
-                for (int i = 0; i < 64; i += 2) {
+                for (int i = 0; i < 32; i += 2) {
                     fma2(s[i], s[i + 1], s[i], s[i + 1], c, -lse2);
                     s[i] = exp2_fast(s[i]);
                     s[i + 1] = exp2_fast(s[i + 1]);
@@ -309,23 +278,22 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                 ok = warp_wait(dp_bar, j & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                load64(lanes + TM_DP + 64 * grp, d);
+                load32(lanes + TM_DP + 32 * grp, d);
 #pragma unroll
-                for (int i = 0; i < 64; ++i) d[i] = s[i] * (d[i] - delta);
+                for (int i = 0; i < 32; ++i) d[i] = s[i] * (d[i] - delta);
                 if ((j + 1) * kRows > open) {
-                    const int lim = mine - j * kRows - 64 * grp;
+                    const int lim = mine - j * kRows - 32 * grp;
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) d[i] = i < lim ? d[i] : 0.f;
+                    for (int i = 0; i < 32; ++i) d[i] = i < lim ? d[i] : 0.f;
                 }
-                store64(lanes + TM_DP + 64 * grp, d);
-                tc_fence_before();
-                mbar_arrive(ds_bar);
+                store32(lanes + TM_DP + 32 * grp, d);
+                warp_arrive(ds_bar, lane);
             }
-            if (ok && n > 0) ok = mbar_wait(done_bar, 0, abort_flag, kWaitNs);
+            if (ok && n > 0) ok = wait_phase(done_bar, 0, abort_flag);
             ok = __all_sync(~0u, ok);
             if (ok) {
                 tc_fence_after();
-                constexpr int W = DP / 2;
+                constexpr int W = DP / 4;
                 store_rows<W>(lanes + TM_DQ + grp * W, n > 0, p.scale,
                               smem + warp * 32 * W * 2, lane, grp * W, p.a.D, [&](int r) -> bf16* {
                                   const int rr = (warp & 3) * 32 + r, t = first + rr / G;
@@ -339,7 +307,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
     __syncthreads();
     tc_fence_after();
     if (threadIdx.x == 0 && *abort_flag) raise_error(p.err, MOE_ERR_TIMEOUT);
-    if (warp == 8) tmem_dealloc(tmem, 512);
+    if (warp == kCompute) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------- dk, dv
@@ -373,8 +341,8 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
         for (int i = 0; i < 10; ++i) mbar_init(bars + 8 * i, 1);
         mbar_init(r_full(0), 32);
         mbar_init(r_full(1), 32);
-        mbar_init(r_empty(0), kCompute / 32);
-        mbar_init(r_empty(1), kCompute / 32);
+        mbar_init(r_empty(0), kCompute);
+        mbar_init(r_empty(1), kCompute);
         mbar_init(kv_bar, 1);
         mbar_init(s_bar, 1);
         mbar_init(p_bar, kCompute);
@@ -384,24 +352,24 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 8) {
+    if (warp == kCompute) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
     pdl_wait();
     pdl_trigger();
-    const int hk = blockIdx.y, tpt = p.tpt, G = p.a.Hq / p.a.Hkv;
+    const int hk = blockIdx.x % p.a.Hkv, tpt = p.tpt, G = p.a.Hq / p.a.Hkv;
     if (warp == 0) {
         int b = -1, item = 0, items = 0;
         if ((sK & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
         const bool skip = __any_sync(~0u, has_error(p.err));
-        if (skip || !find_tile(p.s, true, kRows, blockIdx.x, lane, b, item, items, p.err)) b = -1;
+        if (skip || !find_tile(p.s, true, kRows, blockIdx.x / p.a.Hkv, lane, b, item, items, p.err)) b = -1;
         if (lane == 0) {
             found[0] = b;
             found[1] = item;  // the first keys of a sequence are seen most, and come first
         }
     }
-    if (warp == 1 && blockIdx.x == 0 && hk == 0) check_sequences(p.s, lane, p.err);
+    if (warp == 1 && blockIdx.x == 0) check_sequences(p.s, lane, p.err);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -416,7 +384,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
         const int n = max(0, (nq + tpt - 1) / tpt - i0);
         const auto rows_of = [&](int i) { return G * min(tpt, nq - (i0 + i) * tpt); };
 
-        if (warp == 9) {
+        if (warp == kCompute + 1) {
             if (lane == 0 && n > 0) {
                 const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int h, int t) {
                     for (int c = 0; c < C::PIECES; ++c)
@@ -429,14 +397,14 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
                 for (int i = 0; i < n; ++i) {
                     const int t = q0 + (i0 + i) * tpt;
                     int s = i % C::R0;
-                    if (i >= C::R0 && !mbar_wait(q_empty(s), (i / C::R0 - 1) & 1, abort_flag, kWaitNs))
+                    if (i >= C::R0 && !wait_phase(q_empty(s), (i / C::R0 - 1) & 1, abort_flag))
                         break;
                     mbar_arrive_expect_tx(q_full(s), qbytes);
                     load(sQ + s * C::TILE, &mapQ, q_full(s), hk * G, t);
                     ++iq;
                     if (i == 0) load(sV, &mapV, kv_bar, hk, k0 + kv0);
                     s = i % C::R1;
-                    if (i >= C::R1 && !mbar_wait(do_empty(s), (i / C::R1 - 1) & 1, abort_flag, kWaitNs))
+                    if (i >= C::R1 && !wait_phase(do_empty(s), (i / C::R1 - 1) & 1, abort_flag))
                         break;
                     mbar_arrive_expect_tx(do_full(s), qbytes);
                     load(sDO + s * C::TILE, &mapDO, do_full(s), hk * G, t);
@@ -447,7 +415,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
                 for (int i = max(0, iq - C::R0); i < iq; ++i) drain(q_full(i % C::R0), (i / C::R0) & 1);
                 for (int i = max(0, id - C::R1); i < id; ++i) drain(do_full(i % C::R1), (i / C::R1) & 1);
             }
-        } else if (warp == 10) {
+        } else if (warp == kCompute + 2) {
             // lse and delta of each query tile's rows; a row past the sequence or without
             // a key has lse +inf (its weights are 0) and delta 0
             for (int i = 0; i < n; ++i) {
@@ -464,18 +432,19 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
                 }
                 mbar_arrive(r_full(i & 1));
             }
-        } else if (warp == 8) {
-            const int ksteps = (p.a.D + 15) / 16;
-            const uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_g = idesc_bf16(128, 16 * ksteps, 0, 1);
+        } else if (warp == kCompute) {
+            constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_g = idesc_bf16(128, DP, 0, 1);
             // S^T_i, once its queries are there (rows past them zeroed: dK sums over them)
             const auto scores = [&](int i) -> bool {
                 const int s = i % C::R0;
                 if (!warp_wait(q_full(s), (i / C::R0) & 1, abort_flag)) return false;
                 if (rows_of(i) < kRows) zero_tail(sQ + s * C::TILE, C::PIECES, rows_of(i), lane);
                 tc_fence_after();
-                if (lane == 0) {
-                    for (int k = 0; k < ksteps; ++k)
-                        mma_bf16(tmem + TM_S, desc_k(sK, k), desc_k(sQ + s * C::TILE, k), id_s, k > 0);
+                const uint64_t ad = desc_d(sK), bd = desc_d(sQ + s * C::TILE);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k)
+                        mma_bf16(tmem + TM_S, ad + kd(k), bd + kd(k), id_s, k > 0);
                     mma_commit(s_bar);
                 }
                 __syncwarp();
@@ -488,59 +457,63 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
                 if (!ok) break;
                 if (rows_of(i) < kRows) zero_tail(sDO + sd * C::TILE, C::PIECES, rows_of(i), lane);
                 tc_fence_after();
-                if (lane == 0) {
-                    for (int k = 0; k < ksteps; ++k)
-                        mma_bf16(tmem + TM_DP, desc_k(sV, k), desc_k(sDO + sd * C::TILE, k), id_s,
-                                 k > 0);
+                const uint64_t vd = desc_d(sV), dod = desc_d(sDO + sd * C::TILE);
+                const uint64_t dor = desc_r(sDO + sd * C::TILE), qr = desc_r(sQ + sq * C::TILE);
+                const uint32_t de = do_empty(sd), qe = q_empty(sq), add = i > 0;
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k)
+                        mma_bf16(tmem + TM_DP, vd + kd(k), dod + kd(k), id_s, k > 0);
                     mma_commit(dp_bar);
                 }
                 __syncwarp();
                 ok = warp_wait(p_bar, i & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
+#pragma unroll
                     for (int k = 0; k < kRows / 16; ++k)
-                        mma_bf16_ta(tmem + TM_DV, operand(tmem + TM_S, k),
-                                    desc_mn(sDO + sd * C::TILE, k), id_g, (i | k) != 0);
-                    mma_commit(do_empty(sd));
+                        mma_bf16_ta(tmem + TM_DV, operand(tmem + TM_S, k), dor + kr(k), id_g,
+                                    k > 0 ? 1u : add);
+                    mma_commit(de);
                 }
                 __syncwarp();
                 if (i + 1 < n) ok = scores(i + 1);
                 ok = ok && warp_wait(ds_bar, i & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
+#pragma unroll
                     for (int k = 0; k < kRows / 16; ++k)
-                        mma_bf16_ta(tmem + TM_DK, operand(tmem + TM_DP, k),
-                                    desc_mn(sQ + sq * C::TILE, k), id_g, (i | k) != 0);
-                    mma_commit(q_empty(sq));
+                        mma_bf16_ta(tmem + TM_DK, operand(tmem + TM_DP, k), qr + kr(k), id_g,
+                                    k > 0 ? 1u : add);
+                    mma_commit(qe);
                 }
                 __syncwarp();
             }
-            if (lane == 0) {
-                mma_commit(done_bar);
-                drain(done_bar, 0);
-            }
+            if (elect_one()) mma_commit(done_bar);
             __syncwarp();
-        } else if (warp < 8) {
+            drain(done_bar, 0);
+            __syncwarp();
+        } else if (warp < kCompute) {
             const int grp = warp >> 2, row = threadIdx.x & 127;
             const int key = kv0 + row;  // in its sequence
             const float c = p.scale * kLog2e;
             const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
             bool ok = true;
             for (int i = 0; i < n; ++i) {
-                const float* rd = rowdata + (i & 1) * 256 + 64 * grp;
+                const float* rd = rowdata + (i & 1) * 256 + 32 * grp;
                 // the first token of the tile that sees this key, as the first such column
-                const int from = p.s.causal ? (key - (nk - nq) - (i0 + i) * tpt) * G - 64 * grp : 0;
+                const int from = p.s.causal ? (key - (nk - nq) - (i0 + i) * tpt) * G - 32 * grp : 0;
                 const bool diag = p.s.causal && kv0 + kRows - 1 - (nk - nq) > (i0 + i) * tpt;
                 ok = warp_wait(r_full(i & 1), (i >> 1) & 1, abort_flag) &&
                      warp_wait(s_bar, i & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                float s[64], d[64];
-                load64(lanes + TM_S + 64 * grp, s);
+                float s[32], d[32];
+                load32(lanes + TM_S + 32 * grp, s);
 #pragma unroll
-                for (int q = 0; q < 64; q += 4) {
+                for (int q = 0; q < 32; q += 4) {
                     const float4 e = *reinterpret_cast<const float4*>(rd + q);
                     s[q] = exp2_fast(fmaf(s[q], c, -e.x));
                     s[q + 1] = exp2_fast(fmaf(s[q + 1], c, -e.y));
@@ -549,17 +522,16 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
                 }
                 if (diag) {
 #pragma unroll
-                    for (int q = 0; q < 64; ++q) s[q] = q >= from ? s[q] : 0.f;
+                    for (int q = 0; q < 32; ++q) s[q] = q >= from ? s[q] : 0.f;
                 }
-                store64(lanes + TM_S + 64 * grp, s);
-                tc_fence_before();
-                mbar_arrive(p_bar);
+                store32(lanes + TM_S + 32 * grp, s);
+                warp_arrive(p_bar, lane);
                 ok = warp_wait(dp_bar, i & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                load64(lanes + TM_DP + 64 * grp, d);
+                load32(lanes + TM_DP + 32 * grp, d);
 #pragma unroll
-                for (int q = 0; q < 64; q += 4) {
+                for (int q = 0; q < 32; q += 4) {
                     const float4 e = *reinterpret_cast<const float4*>(rd + 128 + q);
                     d[q] = s[q] * (d[q] - e.x);
                     d[q + 1] = s[q + 1] * (d[q + 1] - e.y);
@@ -568,24 +540,25 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
                 }
                 if (diag) {
 #pragma unroll
-                    for (int q = 0; q < 64; ++q) d[q] = q >= from ? d[q] : 0.f;
+                    for (int q = 0; q < 32; ++q) d[q] = q >= from ? d[q] : 0.f;
                 }
-                store64(lanes + TM_DP + 64 * grp, d);
-                tc_fence_before();
-                mbar_arrive(ds_bar);
-                __syncwarp();
+                store32(lanes + TM_DP + 32 * grp, d);
+                warp_arrive(ds_bar, lane);
                 if (lane == 0) mbar_arrive(r_empty(i & 1));
             }
-            if (ok && n > 0) ok = mbar_wait(done_bar, 0, abort_flag, kWaitNs);
+            if (ok && n > 0) ok = wait_phase(done_bar, 0, abort_flag);
             ok = __all_sync(~0u, ok);
             if (ok) {
                 tc_fence_after();
-                const Heads& dst = grp == 0 ? p.dv : p.dk;
-                store_rows<DP>(lanes + (grp == 0 ? TM_DV : TM_DK), n > 0, grp == 0 ? 1.f : p.scale,
-                               smem + warp * 32 * DP * 2, lane, 0, p.a.D, [&](int r) -> bf16* {
-                                   const int k = kv0 + (warp & 3) * 32 + r;
-                                   return k < nk ? dst.row(k0 + k, hk) : nullptr;
-                               });
+                // groups 0 and 1: the halves of dv; 2 and 3: of dk
+                constexpr int W = DP / 2;
+                const Heads& dst = grp < 2 ? p.dv : p.dk;
+                store_rows<W>(lanes + (grp < 2 ? TM_DV : TM_DK) + (grp & 1) * W, n > 0,
+                              grp < 2 ? 1.f : p.scale, smem + warp * 32 * W * 2, lane, (grp & 1) * W,
+                              p.a.D, [&](int r) -> bf16* {
+                                  const int k = kv0 + (warp & 3) * 32 + r;
+                                  return k < nk ? dst.row(k0 + k, hk) : nullptr;
+                              });
             }
         }
     }
@@ -593,7 +566,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
     __syncthreads();
     tc_fence_after();
     if (threadIdx.x == 0 && *abort_flag) raise_error(p.err, MOE_ERR_TIMEOUT);
-    if (warp == 8) tmem_dealloc(tmem, 512);
+    if (warp == kCompute) tmem_dealloc(tmem, 512);
 }
 
 template <int DP>
@@ -620,7 +593,7 @@ cudaError_t backward(const Attention& p, cudaStream_t st) {
                                              C::SMEM_Q);
         if (e != cudaSuccess) return e;
         LaunchScope ls("attention_dq", st);
-        e = launch_k(kfn, dim3(static_cast<unsigned>(qi), p.a.Hkv), dim3(kThreads), C::SMEM_Q, st,
+        e = launch_k(kfn, dim3(static_cast<unsigned>(qi * p.a.Hkv)), dim3(kThreads), C::SMEM_Q, st,
                      mq, md, mk, mv, prm);
         if (e != cudaSuccess) return e;
     }
@@ -631,7 +604,7 @@ cudaError_t backward(const Attention& p, cudaStream_t st) {
                                                C::SMEM_KV);
     if (e != cudaSuccess) return e;
     LaunchScope ls("attention_dkv", st);
-    return launch_k(kfn, dim3(static_cast<unsigned>(ki), p.a.Hkv), dim3(kThreads), C::SMEM_KV, st,
+    return launch_k(kfn, dim3(static_cast<unsigned>(ki * p.a.Hkv)), dim3(kThreads), C::SMEM_KV, st,
                     mq, md, mk, mv, prm);
 }
 

@@ -17,13 +17,6 @@ constexpr int kRows = 128;
 constexpr int kPiece = kRows * 128;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int k) {  // K-major, k-th 16 of D
-    return sdesc_sw128(tile + (k >> 2) * kPiece + (k & 3) * 32, 16, 1024);
-}
-__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int k) {  // MN-major, k-th 16 rows
-    return sdesc_sw128(tile + k * 2048, kPiece, 1024);
-}
-
 // D[tmem] (+)= A[tmem] * B[smem]: A is M = 128 lanes of 16-bit pairs, 8 columns per 16 of K.
 __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
                                             uint32_t idesc, uint32_t accumulate) {
@@ -34,6 +27,26 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+
+// One lane of a converged warp (the same one every time), in the form that lets the
+// tensor-core instructions take their operands from uniform registers: with 16 busy warps
+// beside the issuing one, a 128 x 128 x 16 product took 333 cycles to issue under
+// `lane == 0` with a descriptor built per step, 121 under elect.sync, and 81 with a step
+// as a constant added to a descriptor (64 is the tensor cores' own time).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(p)
+                 :
+                 : "memory");
+    return p != 0;
+}
+// Descriptors of a tile: K-major (K = D; the k-th 16 of K is kd(k) further) and MN-major
+// (K = rows; the k-th 16 rows are kr(k) further).
+__device__ __forceinline__ uint64_t desc_d(uint32_t tile) { return sdesc_sw128(tile, 16, 1024); }
+__device__ __forceinline__ uint64_t desc_r(uint32_t tile) { return sdesc_sw128(tile, kPiece, 1024); }
+__device__ __forceinline__ constexpr uint64_t kd(int k) { return ((k >> 2) * kPiece + (k & 3) * 32) / 16; }
+__device__ __forceinline__ constexpr uint64_t kr(int k) { return k * 2048 / 16; }
 
 // 32 columns of this warp's 32 TMEM lanes, written from registers.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
@@ -46,6 +59,24 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
         "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
         "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
         "r"(v[30]), "r"(v[31]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+          "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+        "r"(taddr)
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() {
@@ -83,16 +114,93 @@ __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
         : "f"(a0), "f"(a1));
 }
 
-// A wait of every lane of a warp; false (for all of them) when it ran out or another
-// role has given up.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Named barrier over `n` threads, and one that also ORs a predicate.
+__device__ __forceinline__ void bar_sync(int id, int n) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ bool bar_or(int id, int n, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(n)
+        : "memory");
+    return r != 0;
+}
+// One arrival for a warp whose lanes' earlier TMEM accesses are waited for.
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+
+// Waits for a phase; false when kWaitNs ran out or another role has given up. The roles
+// hand tiles over every few hundred cycles, so the polls are plain try_waits without a
+// suspend hint (a suspended warp woke late), and the clock is read every 64 polls only.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if ((i & 63u) != 0) continue;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (*abort) return false;
+        if (t - t0 > kWaitNs) {
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+// The same by every lane of a warp, with one answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, kWaitNs));
+    return __all_sync(0xffffffffu, wait_phase(bar, parity, abort));
 }
 // Bounded wait for something in flight before leaving (given up or not).
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait_sleep(bar, parity, 20000u))
         if (globaltimer_ns() - t0 > kWaitNs) break;
+}
+
+// 32 rows x W columns (fp32, TMEM columns t ..) of one warp, times f, as bf16 rows:
+// row(r) gives the row's destination or nullptr. stg: 32 x W x 2 bytes of shared memory.
+template <int W, class Row>
+__device__ __forceinline__ void store_rows(uint32_t t, bool any, float f, uint8_t* stg, int lane,
+                                           int col0, int D, Row row) {
+    constexpr int CH = W / 8;
+#pragma unroll
+    for (int q = 0; q < W; q += 16) {
+        uint32_t o[16];
+        if (any) {
+            tmem_ld16(t + q, o);
+            tmem_ld_wait();
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = any && f != 0.f ? __uint_as_float(o[8 * i + e]) * f : 0.f;
+            *reinterpret_cast<uint4*>(stg + lane * W * 2 + ((q / 8 + i) ^ (lane & (CH - 1))) * 16) =
+                pack8(v);
+        }
+    }
+    __syncwarp();
+    constexpr int RPI = 32 / CH;
+#pragma unroll 4
+    for (int i = 0; i < 32; i += RPI) {
+        const int rl = i + lane / CH, ch = lane % CH;
+        bf16* dst = row(rl);
+        if (dst != nullptr && col0 + ch * 8 < D)
+            *reinterpret_cast<uint4*>(dst + col0 + ch * 8) =
+                *reinterpret_cast<const uint4*>(stg + rl * W * 2 + (ch ^ (rl & (CH - 1))) * 16);
+    }
 }
 
 // Zeroes rows [first, 128) of a tile (whole 128-byte rows of each piece, so the swizzle
