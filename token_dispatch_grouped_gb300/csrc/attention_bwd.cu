@@ -30,7 +30,9 @@ namespace moe {
 namespace attn {
 namespace {
 
-constexpr int kCompute = 16;  // warps: four groups of four, 32 columns of every row each
+constexpr int kGroups = 4;            // of four warps, kCols columns of every row each
+constexpr int kCols = kRows / kGroups;
+constexpr int kCompute = 4 * kGroups;  // warps
 constexpr int kThreads = (kCompute + 3) * 32;  // and tensor cores, TMA, row data
 constexpr float kLog2e = 1.44269504088896341f;
 
@@ -55,22 +57,29 @@ struct Cfg {
     static constexpr int SMEM_KV = TILES + 2 * 2 * 512 + 256;  // two slots of lse and delta
 };
 
-// 32 columns of TMEM as fp32.
-__device__ __forceinline__ void load32(uint32_t t, float (&v)[32]) {
-    tmem_ld32(t, *reinterpret_cast<uint32_t(*)[32]>(v));
+// A group's columns of TMEM as fp32.
+__device__ __forceinline__ void load_cols(uint32_t t, float (&v)[kCols]) {
+#pragma unroll
+    for (int i = 0; i < kCols; i += 32) tmem_ld32(t + i, *reinterpret_cast<uint32_t(*)[32]>(v + i));
     tmem_ld_wait();
 }
-// 32 fp32 values as 16 columns of bf16 pairs.
-__device__ __forceinline__ void store32(uint32_t t, const float (&v)[32]) {
-    uint32_t w[16];
+// A group's columns as kCols / 2 columns of bf16 pairs.
+__device__ __forceinline__ void store_cols(uint32_t t, const float (&v)[kCols]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1]);
-    tmem_st16(t, w);
+    for (int h = 0; h < kCols; h += 32) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = pack2(v[h + 2 * i], v[h + 2 * i + 1]);
+        tmem_st16(t + h / 2, w);
+    }
     tmem_st_wait();
 }
-// k-th 16 columns of a bf16 operand that the groups wrote: group g's 32 columns in the
-// 16 TMEM columns at t + 32 g, over scores that it has read itself.
-__device__ __forceinline__ uint32_t operand(uint32_t t, int k) { return t + 32 * (k >> 1) + 8 * (k & 1); }
+// k-th 16 columns of a bf16 operand that the groups wrote: group g's columns in the
+// kCols / 2 TMEM columns at t + kCols g, over scores that it has read itself.
+__device__ __forceinline__ uint32_t operand(uint32_t t, int k) {
+    constexpr int per = kCols / 16;
+    return t + kCols * (k / per) + 8 * (k % per);
+}
 
 // ---------------------------------------------------------------------- dq
 template <int DP>
@@ -241,8 +250,8 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                 const bf16* o = p.out.row(q0 + token, hk * G + g);
                 const bf16* d = p.dout.row(q0 + token, hk * G + g);
 #pragma unroll
-                for (int i = 0; i < DP / 32; ++i) {
-                    const int col = grp * (DP / 4) + i * 8;
+                for (int i = 0; i < DP / kGroups / 8; ++i) {
+                    const int col = grp * (DP / kGroups) + i * 8;
                     if (col >= p.a.D) break;
                     float x[8], y[8];
                     unpack8(*reinterpret_cast<const uint4*>(o + col), x);
@@ -255,8 +264,9 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
             }
             part_delta[grp * 128 + row] = delta;
             bar_sync(1, kCompute * 32);
-            delta = (part_delta[row] + part_delta[128 + row]) +
-                    (part_delta[256 + row] + part_delta[384 + row]);
+            delta = part_delta[row];
+#pragma unroll
+            for (int i = 1; i < kGroups; ++i) delta += part_delta[i * 128 + row];
             if (valid && grp == 0) {
                 const long long at = (static_cast<long long>(hk) * p.s.Tq + q0 + token) * G + g;
                 p.row_lse[at] = lse2;
@@ -267,10 +277,10 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                 ok = warp_wait(s_bar(j & 1), (j >> 1) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                float s[32], d[32];
-                load32(lanes + TM_S + 128 * (j & 1) + 32 * grp, s);
+                float s[kCols], d[kCols];
+                load_cols(lanes + TM_S + 128 * (j & 1) + kCols * grp, s);
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
+                for (int i = 0; i < kCols; i += 2) {
                     fma2(s[i], s[i + 1], s[i], s[i + 1], c, -lse2);
                     s[i] = exp2_fast(s[i]);
                     s[i + 1] = exp2_fast(s[i + 1]);
@@ -278,22 +288,22 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                 ok = warp_wait(dp_bar, j & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                load32(lanes + TM_DP + 32 * grp, d);
+                load_cols(lanes + TM_DP + kCols * grp, d);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) d[i] = s[i] * (d[i] - delta);
+                for (int i = 0; i < kCols; ++i) d[i] = s[i] * (d[i] - delta);
                 if ((j + 1) * kRows > open) {
-                    const int lim = mine - j * kRows - 32 * grp;
+                    const int lim = mine - j * kRows - kCols * grp;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) d[i] = i < lim ? d[i] : 0.f;
+                    for (int i = 0; i < kCols; ++i) d[i] = i < lim ? d[i] : 0.f;
                 }
-                store32(lanes + TM_DP + 32 * grp, d);
+                store_cols(lanes + TM_DP + kCols * grp, d);
                 warp_arrive(ds_bar, lane);
             }
             if (ok && n > 0) ok = wait_phase(done_bar, 0, abort_flag);
             ok = __all_sync(~0u, ok);
             if (ok) {
                 tc_fence_after();
-                constexpr int W = DP / 4;
+                constexpr int W = DP / kGroups;
                 store_rows<W>(lanes + TM_DQ + grp * W, n > 0, p.scale,
                               smem + warp * 32 * W * 2, lane, grp * W, p.a.D, [&](int r) -> bf16* {
                                   const int rr = (warp & 3) * 32 + r, t = first + rr / G;
@@ -502,18 +512,18 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
             const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
             bool ok = true;
             for (int i = 0; i < n; ++i) {
-                const float* rd = rowdata + (i & 1) * 256 + 32 * grp;
+                const float* rd = rowdata + (i & 1) * 256 + kCols * grp;
                 // the first token of the tile that sees this key, as the first such column
-                const int from = p.s.causal ? (key - (nk - nq) - (i0 + i) * tpt) * G - 32 * grp : 0;
+                const int from = p.s.causal ? (key - (nk - nq) - (i0 + i) * tpt) * G - kCols * grp : 0;
                 const bool diag = p.s.causal && kv0 + kRows - 1 - (nk - nq) > (i0 + i) * tpt;
                 ok = warp_wait(r_full(i & 1), (i >> 1) & 1, abort_flag) &&
                      warp_wait(s_bar, i & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                float s[32], d[32];
-                load32(lanes + TM_S + 32 * grp, s);
+                float s[kCols], d[kCols];
+                load_cols(lanes + TM_S + kCols * grp, s);
 #pragma unroll
-                for (int q = 0; q < 32; q += 4) {
+                for (int q = 0; q < kCols; q += 4) {
                     const float4 e = *reinterpret_cast<const float4*>(rd + q);
                     s[q] = exp2_fast(fmaf(s[q], c, -e.x));
                     s[q + 1] = exp2_fast(fmaf(s[q + 1], c, -e.y));
@@ -522,16 +532,16 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
                 }
                 if (diag) {
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) s[q] = q >= from ? s[q] : 0.f;
+                    for (int q = 0; q < kCols; ++q) s[q] = q >= from ? s[q] : 0.f;
                 }
-                store32(lanes + TM_S + 32 * grp, s);
+                store_cols(lanes + TM_S + kCols * grp, s);
                 warp_arrive(p_bar, lane);
                 ok = warp_wait(dp_bar, i & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                load32(lanes + TM_DP + 32 * grp, d);
+                load_cols(lanes + TM_DP + kCols * grp, d);
 #pragma unroll
-                for (int q = 0; q < 32; q += 4) {
+                for (int q = 0; q < kCols; q += 4) {
                     const float4 e = *reinterpret_cast<const float4*>(rd + 128 + q);
                     d[q] = s[q] * (d[q] - e.x);
                     d[q + 1] = s[q + 1] * (d[q + 1] - e.y);
@@ -540,9 +550,9 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
                 }
                 if (diag) {
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) d[q] = q >= from ? d[q] : 0.f;
+                    for (int q = 0; q < kCols; ++q) d[q] = q >= from ? d[q] : 0.f;
                 }
-                store32(lanes + TM_DP + 32 * grp, d);
+                store_cols(lanes + TM_DP + kCols * grp, d);
                 warp_arrive(ds_bar, lane);
                 if (lane == 0) mbar_arrive(r_empty(i & 1));
             }
@@ -550,11 +560,12 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
             ok = __all_sync(~0u, ok);
             if (ok) {
                 tc_fence_after();
-                // groups 0 and 1: the halves of dv; 2 and 3: of dk
-                constexpr int W = DP / 2;
-                const Heads& dst = grp < 2 ? p.dv : p.dk;
-                store_rows<W>(lanes + (grp < 2 ? TM_DV : TM_DK) + (grp & 1) * W, n > 0,
-                              grp < 2 ? 1.f : p.scale, smem + warp * 32 * W * 2, lane, (grp & 1) * W,
+                // the first half of the groups: parts of dv; the others: of dk
+                constexpr int PER = kGroups / 2, W = DP / PER;
+                const bool is_v = grp < PER;
+                const Heads& dst = is_v ? p.dv : p.dk;
+                store_rows<W>(lanes + (is_v ? TM_DV : TM_DK) + (grp % PER) * W, n > 0,
+                              is_v ? 1.f : p.scale, smem + warp * 32 * W * 2, lane, (grp % PER) * W,
                               p.a.D, [&](int r) -> bf16* {
                                   const int k = kv0 + (warp & 3) * 32 + r;
                                   return k < nk ? dst.row(k0 + k, hk) : nullptr;
