@@ -17,9 +17,10 @@
 // groups of four warps that turn scores into weights, each for 32 of the 128 columns of
 // every row (with two groups of 64 columns the tensor cores waited for them: 1.67 and 1.94
 // million cycles a SM for dq and dkv of 8192 tokens, 32/8 heads of 128, against XXX);
-// P and dS go back to TMEM as bf16 operands over the columns that their group has read. The order of the products (dP, [P] dV, next S, [dS] dK) leaves the tensor
-// cores work while the other warps compute: P while dP runs, dS while dV and the next S
-// run. TMEM: dq_kernel S twice, dP, dQ; dkv_kernel S, dP, dV, dK (4 x 128 columns).
+// P and dS go back to TMEM as bf16 operands over the columns that their group has read. The order of the products leaves the tensor cores work while the other warps
+// compute: in dkv_kernel (dP, [P] dV, next S, [dS] dK) P while dP runs and dS while dV and
+// the next S run; in dq_kernel the next S and dP run while dS is formed. TMEM: dq_kernel
+// S, dP twice, dQ; dkv_kernel S, dP, dV, dK (4 x 128 columns).
 //
 // P and dS are rounded to bf16 (the operand type), everything else is fp32; scale enters
 // dq and dk once at the end. Masked weights are zero by selection, and rows of an operand
@@ -42,7 +43,7 @@ struct Params {
     float scale;
     Heads out, dout, dq, dk, dv;
     const float* lse;
-    float *row_lse, *row_delta;  // [Hkv][Tq][G]: lse * log2(e) (+inf: no key) and delta
+    float *row_lse, *row_delta;  // [Hkv][Tq][G]: -lse * log2(e) (-inf: no key) and -delta
     int* err;
     int tpt;  // tokens of a 128-row query tile
 };
@@ -98,22 +99,23 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
     const auto k_empty = [&](int s) { return bars + 8u * (3 + s); };
     const auto v_full = [&](int s) { return bars + 8u * (6 + s); };
     const auto v_empty = [&](int s) { return bars + 8u * (8 + s); };
-    const auto s_bar = [&](int s) { return bars + 8u * (10 + s); };
-    const uint32_t q_bar = bars + 96, do_bar = bars + 104, dp_bar = bars + 112,
-                   ds_bar = bars + 120, done_bar = bars + 128;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 136);
+    const auto dp_bar = [&](int s) { return bars + 8u * (10 + s); };
+    const uint32_t q_bar = bars + 96, do_bar = bars + 104, s_bar = bars + 112,
+                   ds_bar = bars + 120, done_bar = bars + 128, s_read = bars + 136;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 144);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* found = reinterpret_cast<int*>(tmem_slot + 2);
-    constexpr uint32_t TM_S = 0, TM_DP = 256, TM_DQ = 384;
+    constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DQ = 384;  // dP twice
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 12; ++i) mbar_init(bars + 8 * i, 1);
         mbar_init(q_bar, 1);
         mbar_init(do_bar, 1);
-        mbar_init(dp_bar, 1);
+        mbar_init(s_bar, 1);
         mbar_init(ds_bar, kCompute);
         mbar_init(done_bar, 1);
+        mbar_init(s_read, kCompute);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -183,7 +185,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
             }
         } else if (warp == kCompute) {
             constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_q = idesc_bf16(128, DP, 0, 1);
-            // S_j, once its keys are there
+            // S_j and dP_j, once their keys and values are there
             const auto scores = [&](int j) -> bool {
                 const int s = j % C::R0;
                 if (!warp_wait(k_full(s), (j / C::R0) & 1, abort_flag)) return false;
@@ -191,42 +193,47 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                     zero_tail(sK + s * C::TILE, C::PIECES, seen - j * kRows, lane);
                 tc_fence_after();
                 const uint64_t ad = desc_d(sQ), bd = desc_d(sK + s * C::TILE);
-                const uint32_t dst = tmem + TM_S + 128 * (j & 1), bar = s_bar(j & 1);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k)
+                        mma_bf16(tmem + TM_S, ad + kd(k), bd + kd(k), id_s, k > 0);
+                    mma_commit(s_bar);
+                }
+                __syncwarp();
+                return true;
+            };
+            const auto dprob = [&](int j) -> bool {
+                const int s = j % C::R1;
+                if (!warp_wait(v_full(s), (j / C::R1) & 1, abort_flag)) return false;
+                tc_fence_after();
+                const uint64_t ad = desc_d(sDO), bd = desc_d(sV + s * C::TILE);
+                const uint32_t dst = tmem + TM_DP + 128 * (j & 1), bar = dp_bar(j & 1), ve = v_empty(s);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < DP / 16; ++k) mma_bf16(dst, ad + kd(k), bd + kd(k), id_s, k > 0);
                     mma_commit(bar);
+                    mma_commit(ve);
                 }
                 __syncwarp();
                 return true;
             };
             bool ok = n == 0 || (warp_wait(q_bar, 0, abort_flag) && scores(0) &&
-                                 warp_wait(do_bar, 0, abort_flag));
+                                 warp_wait(do_bar, 0, abort_flag) && dprob(0));
             for (int j = 0; j < n && ok; ++j) {
-                const int sv = j % C::R1, sk = j % C::R0;
-                ok = warp_wait(v_full(sv), (j / C::R1) & 1, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t dod = desc_d(sDO), vd = desc_d(sV + sv * C::TILE);
-                const uint32_t ve = v_empty(sv);
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < DP / 16; ++k)
-                        mma_bf16(tmem + TM_DP, dod + kd(k), vd + kd(k), id_s, k > 0);
-                    mma_commit(dp_bar);
-                    mma_commit(ve);
-                }
-                __syncwarp();
-                if (j + 1 < n) ok = scores(j + 1);
+                const int sk = j % C::R0;
+                // the next tile's products run while dS_j is formed: S may be overwritten
+                // once it is in registers, and dP has two places
+                if (j + 1 < n)
+                    ok = warp_wait(s_read, j & 1, abort_flag) && scores(j + 1) && dprob(j + 1);
                 ok = ok && warp_wait(ds_bar, j & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t kdesc = desc_r(sK + sk * C::TILE);
-                const uint32_t ke = k_empty(sk), add = j > 0;
+                const uint32_t ke = k_empty(sk), add = j > 0, src = tmem + TM_DP + 128 * (j & 1);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kRows / 16; ++k)
-                        mma_bf16_ta(tmem + TM_DQ, operand(tmem + TM_DP, k), kdesc + kr(k), id_q,
+                        mma_bf16_ta(tmem + TM_DQ, operand(src, k), kdesc + kr(k), id_q,
                                     k > 0 ? 1u : add);
                     mma_commit(ke);
                 }
@@ -245,7 +252,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
             const float c = p.scale * kLog2e;
             const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
             // delta: each group sums a quarter of the row's columns
-            float delta = 0.f, lse2 = INFINITY;
+            float delta = 0.f, neg_lse = -INFINITY;
             if (valid) {
                 const bf16* o = p.out.row(q0 + token, hk * G + g);
                 const bf16* d = p.dout.row(q0 + token, hk * G + g);
@@ -260,43 +267,49 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                     for (int e = 0; e < 8; ++e) delta += x[e] * y[e];
                 }
                 const float e = p.lse[static_cast<long long>(q0 + token) * p.a.Hq + hk * G + g];
-                lse2 = e == -INFINITY ? INFINITY : e * kLog2e;
+                neg_lse = e == -INFINITY ? e : -e * kLog2e;
             }
             part_delta[grp * 128 + row] = delta;
             bar_sync(1, kCompute * 32);
             delta = part_delta[row];
 #pragma unroll
             for (int i = 1; i < kGroups; ++i) delta += part_delta[i * 128 + row];
+            const float neg_delta = -delta;
             if (valid && grp == 0) {
                 const long long at = (static_cast<long long>(hk) * p.s.Tq + q0 + token) * G + g;
-                p.row_lse[at] = lse2;
-                p.row_delta[at] = delta;
+                p.row_lse[at] = neg_lse;
+                p.row_delta[at] = neg_delta;
             }
             bool ok = true;
             for (int j = 0; j < n; ++j) {
-                ok = warp_wait(s_bar(j & 1), (j >> 1) & 1, abort_flag);
+                ok = warp_wait(s_bar, j & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 float s[kCols], d[kCols];
-                load_cols(lanes + TM_S + 128 * (j & 1) + kCols * grp, s);
+                load_cols(lanes + TM_S + kCols * grp, s);
+                warp_arrive(s_read, lane);
 #pragma unroll
                 for (int i = 0; i < kCols; i += 2) {
-                    fma2(s[i], s[i + 1], s[i], s[i + 1], c, -lse2);
+                    fma2v(s[i], s[i + 1], c, neg_lse, neg_lse);
                     s[i] = exp2_fast(s[i]);
                     s[i + 1] = exp2_fast(s[i + 1]);
                 }
-                ok = warp_wait(dp_bar, j & 1, abort_flag);
+                ok = warp_wait(dp_bar(j & 1), (j >> 1) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                load_cols(lanes + TM_DP + kCols * grp, d);
+                const uint32_t tD = lanes + TM_DP + 128 * (j & 1) + kCols * grp;
+                load_cols(tD, d);
 #pragma unroll
-                for (int i = 0; i < kCols; ++i) d[i] = s[i] * (d[i] - delta);
+                for (int i = 0; i < kCols; i += 2) {
+                    add2(d[i], d[i + 1], neg_delta, neg_delta);
+                    mul2(d[i], d[i + 1], s[i], s[i + 1]);
+                }
                 if ((j + 1) * kRows > open) {
                     const int lim = mine - j * kRows - kCols * grp;
 #pragma unroll
                     for (int i = 0; i < kCols; ++i) d[i] = i < lim ? d[i] : 0.f;
                 }
-                store_cols(lanes + TM_DP + kCols * grp, d);
+                store_cols(tD, d);
                 warp_arrive(ds_bar, lane);
             }
             if (ok && n > 0) ok = wait_phase(done_bar, 0, abort_flag);
@@ -426,8 +439,8 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
                 for (int i = max(0, id - C::R1); i < id; ++i) drain(do_full(i % C::R1), (i / C::R1) & 1);
             }
         } else if (warp == kCompute + 2) {
-            // lse and delta of each query tile's rows; a row past the sequence or without
-            // a key has lse +inf (its weights are 0) and delta 0
+            // -lse and -delta of each query tile's rows; a row past the sequence or without
+            // a key has -lse = -inf (its weights are 0) and delta 0
             for (int i = 0; i < n; ++i) {
                 if (i >= 2 && !warp_wait(r_empty(i & 1), (i / 2 - 1) & 1, abort_flag)) break;
                 const int rows = rows_of(i);
@@ -437,7 +450,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const int r = u * 32 + lane;
-                    dst[r] = r < rows ? p.row_lse[at + r] : INFINITY;
+                    dst[r] = r < rows ? p.row_lse[at + r] : -INFINITY;
                     dst[128 + r] = r < rows ? p.row_delta[at + r] : 0.f;
                 }
                 mbar_arrive(r_full(i & 1));
@@ -525,10 +538,10 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
 #pragma unroll
                 for (int q = 0; q < kCols; q += 4) {
                     const float4 e = *reinterpret_cast<const float4*>(rd + q);
-                    s[q] = exp2_fast(fmaf(s[q], c, -e.x));
-                    s[q + 1] = exp2_fast(fmaf(s[q + 1], c, -e.y));
-                    s[q + 2] = exp2_fast(fmaf(s[q + 2], c, -e.z));
-                    s[q + 3] = exp2_fast(fmaf(s[q + 3], c, -e.w));
+                    fma2v(s[q], s[q + 1], c, e.x, e.y);
+                    fma2v(s[q + 2], s[q + 3], c, e.z, e.w);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) s[q + u] = exp2_fast(s[q + u]);
                 }
                 if (diag) {
 #pragma unroll
@@ -543,10 +556,10 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
 #pragma unroll
                 for (int q = 0; q < kCols; q += 4) {
                     const float4 e = *reinterpret_cast<const float4*>(rd + 128 + q);
-                    d[q] = s[q] * (d[q] - e.x);
-                    d[q + 1] = s[q + 1] * (d[q + 1] - e.y);
-                    d[q + 2] = s[q + 2] * (d[q + 2] - e.z);
-                    d[q + 3] = s[q + 3] * (d[q + 3] - e.w);
+                    add2(d[q], d[q + 1], e.x, e.y);
+                    add2(d[q + 2], d[q + 3], e.z, e.w);
+                    mul2(d[q], d[q + 1], s[q], s[q + 1]);
+                    mul2(d[q + 2], d[q + 3], s[q + 2], s[q + 3]);
                 }
                 if (diag) {
 #pragma unroll
