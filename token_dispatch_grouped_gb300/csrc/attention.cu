@@ -10,13 +10,18 @@
 // query heads of 128 / G tokens (token-major), so grouped heads share every key and value
 // tile that is loaded, and a short sequence still fills its tiles. Both tiles use each
 // 128-key tile of K and V from shared memory. Roles:
-//   warp 9     loads: Q once, then K and V tiles by TMA into a ring of stages;
+//   warp 9     loads: Q once, then K and V tiles by TMA, two or three in flight of each;
 //   warp 8     the tensor cores: S_x = Q_x K^T (both from shared memory) into TMEM,
 //              O_x += P_x V with P_x as the TMEM operand;
 //   warps 0-3  softmax of tile 0, warps 4-7 of tile 1, one row a thread: S_x to registers,
-//              p as bf16 over S_x's first 64 TMEM columns.
-// While one tile is in softmax the tensor cores run the other tile's products. TMEM:
-// S_0, S_1 (128 columns each), O_0, O_1 (D each), fp32.
+//              p as bf16 over S_x's first 64 TMEM columns, handed over in two halves so
+//              that the first products run while the second half is formed.
+// While one tile is in softmax the tensor cores run the other tile's products (1024 cycles
+// at D = 128). A step lasts as long as one tile's chain of softmax, PV and the next S, so
+// everything that the products do not wait for (the row sums) comes after the hand-over.
+// Two threads a row (16 warps) measured slower (721 against 692 us for 16384 tokens, 16/4
+// heads of 128): the exponentials of a tile share the same units, and more warps slow the
+// issue of the products. TMEM: S_0, S_1 (128 columns each), O_0, O_1 (D each), fp32.
 //
 // m moves only when the new maximum exceeds it by 2^8 in weight (c (max - m) > 8): p stays
 // at most 256, exact in the fp32 sum, and the pass over O in TMEM is rare after the first
@@ -36,8 +41,9 @@ template <int DP>  // D padded to 64 or 128
 struct Cfg {
     static constexpr int PIECES = DP / 64;
     static constexpr int TILE = PIECES * kPiece;
-    static constexpr int STAGES = DP == 128 ? 5 : 8;
-    static constexpr int SMEM = 1024 + 2 * TILE + STAGES * TILE + 256;
+    static constexpr int KR = 3, VR = 2;  // tiles of K and V in shared memory
+    static constexpr int TILES = (2 + KR + VR) * TILE;
+    static constexpr int SMEM = TILES + 256;
     static constexpr uint32_t TM_S = 0, TM_O = 256;
 };
 
@@ -57,36 +63,28 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
                          const __grid_constant__ CUtensorMap mapK,
                          const __grid_constant__ CUtensorMap mapV, const Params p) {
     using C = Cfg<DP>;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    const uint32_t sQ = base, sKV = base + 2 * C::TILE;
-    uint8_t* misc = smem_raw + (base - raw) + (2 + C::STAGES) * C::TILE;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sQ = smem_u32(smem), sK = sQ + 2 * C::TILE, sV = sK + C::KR * C::TILE;
+    uint8_t* misc = smem + C::TILES;
     const uint32_t bars = smem_u32(misc);
-    const auto full = [&](int s) { return bars + 8u * s; };
-    const auto empty = [&](int s) { return bars + 8u * (C::STAGES + s); };
-    const auto q_bar = [&](int x) { return bars + 8u * (2 * C::STAGES + x); };
-    const auto s_bar = [&](int x) { return bars + 8u * (2 * C::STAGES + 2 + x); };  // S_x written
-    const auto p_bar = [&](int x) { return bars + 8u * (2 * C::STAGES + 4 + x); };  // P_x written
-    const auto o_bar = [&](int x) { return bars + 8u * (2 * C::STAGES + 6 + x); };  // O_x final
-    const uint32_t done_bar = bars + 8u * (2 * C::STAGES + 8);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 8 * (2 * C::STAGES + 9));
+    const auto k_full = [&](int s) { return bars + 8u * s; };
+    const auto v_full = [&](int s) { return bars + 8u * (3 + s); };
+    const auto step = [&](int s) { return bars + 8u * (5 + s); };         // step j's products done
+    const auto q_bar = [&](int x) { return bars + 8u * (7 + x); };
+    const auto s_bar = [&](int x) { return bars + 8u * (9 + x); };        // S_x written
+    const auto o_bar = [&](int x) { return bars + 8u * (11 + x); };       // O_x final
+    const auto p_bar = [&](int x, int h) { return bars + 8u * (13 + 2 * x + h); };  // half of P_x
+    const uint32_t done_bar = bars + 8u * 17, tail_bar = bars + 8u * 18;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 8 * 19);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* found = reinterpret_cast<int*>(tmem_slot + 2);  // sequence (-1: none), item
+    Work* found = reinterpret_cast<Work*>(tmem_slot + 2);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(full(s), 1);
-            mbar_init(empty(s), 1);
-        }
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(q_bar(x), 1);
-            mbar_init(s_bar(x), 1);
-            mbar_init(p_bar(x), kRows);
-            mbar_init(o_bar(x), 1);
-        }
+        for (int i = 0; i < 13; ++i) mbar_init(bars + 8 * i, 1);
+        for (int i = 13; i < 17; ++i) mbar_init(bars + 8 * i, 4);  // the tile's warps
         mbar_init(done_bar, 1);
+        mbar_init(tail_bar, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -94,71 +92,87 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
+    if (warp == 9 && lane == 0) {
+        prefetch_tensormap(&mapQ);
+        prefetch_tensormap(&mapK);
+        prefetch_tensormap(&mapV);
+    }
     pdl_wait();
     pdl_trigger();
-    const int hk = blockIdx.y, tpt = p.tpt, G = p.a.Hq / p.a.Hkv;
+    const int hk = blockIdx.x % p.a.Hkv, tpt = p.tpt, G = p.a.Hq / p.a.Hkv;
     if (warp == 0) {
-        int b = -1, item = 0, items = 0;
-        const bool skip = __any_sync(~0u, has_error(p.err));
-        if (skip || !find_tile(p.s, false, 2 * tpt, blockIdx.x, lane, b, item, items, p.err)) b = -1;
-        if (lane == 0) {
-            found[0] = b;
-            found[1] = items - 1 - item;  // the longest rows of a sequence first
-        }
+        if ((sQ & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
+        const bool skip = has_error(p.err);
+        Work w = find_work(p.s, false, 2 * tpt, blockIdx.x / p.a.Hkv, lane, p.err);
+        if (skip) w.items = 0;
+        if (lane == 0) *found = w;
     }
-    if (warp == 1 && blockIdx.x == 0 && hk == 0) check_sequences(p.s, lane, p.err);
+    if (warp == 1 && blockIdx.x == 0) check_sequences(p.s, lane, p.err);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int b = found[0];
-    if (b >= 0) {
-        const int q0 = p.s.cu_q[b], nq = p.s.cu_q[b + 1] - q0;
-        const int k0 = p.s.cu_k[b], nk = p.s.cu_k[b + 1] - k0;
-        const int first[2] = {found[1] * 2 * tpt, found[1] * 2 * tpt + tpt};
-        // keys that some row of tile x sees, and their tiles
-        int limit[2], tiles[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int last = min(first[x] + tpt, nq) - 1;
-            limit[x] = last < first[x] ? 0 : p.s.causal ? max(0, min(nk, last + 1 + nk - nq)) : nk;
-            tiles[x] = (limit[x] + kRows - 1) / kRows;
-        }
-        const int n = max(tiles[0], tiles[1]);
-        const int seen = max(limit[0], limit[1]);
+    const Work w = *found;
+    if (w.items > 0) {
+        const int q0 = w.q0, nq = w.nq, k0 = w.k0, nk = w.nk;
+        const int base = (w.items - 1 - w.item) * 2 * tpt;  // the longest rows first
+        // keys that some row of a tile sees, and their tiles
+        const auto limit_of = [&](int first) {
+            const int last = min(first + tpt, nq) - 1;
+            return last < first ? 0 : p.s.causal ? max(0, min(nk, last + 1 + nk - nq)) : nk;
+        };
+        const int limit0 = limit_of(base), limit1 = limit_of(base + tpt);
+        const int tiles0 = (limit0 + kRows - 1) / kRows, tiles1 = (limit1 + kRows - 1) / kRows;
+        const int n = max(tiles0, tiles1), seen = max(limit0, limit1);
+        const bool ragged = seen % kRows != 0;  // the last V tile has rows past the keys
 
         if (warp == 9) {
             // ------------------------------------------------------------ loads
-            if (lane == 0 && n > 0) {
-                for (int x = 0; x < 2; ++x) {
-                    if (tiles[x] == 0) continue;
-                    mbar_arrive_expect_tx(q_bar(x), C::PIECES * 128 * G * tpt);
+            if (lane == 0) {
+                const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int h, int t) {
                     for (int c = 0; c < C::PIECES; ++c)
-                        tma_load_3d(sQ + x * C::TILE + c * kPiece, &mapQ, q_bar(x), 64 * c, hk * G,
-                                    q0 + first[x]);
-                }
-                int i = 0;
-                for (; i < 2 * n; ++i) {  // K and V tiles in turn
-                    const int slot = i % C::STAGES;
-                    if (i >= C::STAGES &&
-                        !wait_phase(empty(slot), (i / C::STAGES - 1) & 1, abort_flag))
-                        break;
-                    mbar_arrive_expect_tx(full(slot), C::TILE);
-                    for (int c = 0; c < C::PIECES; ++c)
-                        tma_load_3d(sKV + slot * C::TILE + c * kPiece, (i & 1) ? &mapV : &mapK,
-                                    full(slot), 64 * c, hk, k0 + (i >> 1) * kRows);
+                        tma_load_3d(dst + c * kPiece, m, bar, 64 * c, h, t);
+                };
+                const uint32_t qbytes = C::PIECES * 128 * G * tpt;
+                int jk = 0, jv = 0;
+                const auto load_q = [&](int x) {
+                    mbar_arrive_expect_tx(q_bar(x), qbytes);
+                    load(sQ + x * C::TILE, &mapQ, q_bar(x), hk * G, q0 + base + x * tpt);
+                };
+                const auto load_k = [&](int j) {
+                    mbar_arrive_expect_tx(k_full(j % C::KR), C::TILE);
+                    load(sK + j % C::KR * C::TILE, &mapK, k_full(j % C::KR), hk, k0 + j * kRows);
+                    ++jk;
+                };
+                if (tiles0 > 0) load_q(0);
+                if (n > 0) load_k(0);
+                if (tiles1 > 0) load_q(1);
+                for (int j = 0; j < n; ++j) {
+                    // step j - 2 is the last that reads V_{j-2}; K_{j-2} was read before it
+                    if (j >= 2) wait_phase(step(j & 1), (j / 2 - 1) & 1, abort_flag);
+                    if (*abort_flag) break;
+                    mbar_arrive_expect_tx(v_full(j & 1), C::TILE);
+                    load(sV + (j & 1) * C::TILE, &mapV, v_full(j & 1), hk, k0 + j * kRows);
+                    ++jv;
+                    if (j + 1 < n) load_k(j + 1);
                 }
                 // nothing is in flight when the CTA leaves
-                for (int x = 0; x < 2; ++x)
-                    if (tiles[x] > 0) drain(q_bar(x), 0);
-                for (int j = max(0, i - C::STAGES); j < i; ++j)
-                    drain(full(j % C::STAGES), (j / C::STAGES) & 1);
+                if (tiles0 > 0) drain(q_bar(0), 0);
+                if (tiles1 > 0) drain(q_bar(1), 0);
+                for (int j = max(0, jk - C::KR); j < jk; ++j) drain(k_full(j % C::KR), (j / C::KR) & 1);
+                for (int j = max(0, jv - C::VR); j < jv; ++j) drain(v_full(j & 1), (j >> 1) & 1);
+            }
+            __syncwarp();
+            if (ragged) {
+                // the last V tile has landed (or the CTA has given up)
+                zero_tail(sV + ((n - 1) & 1) * C::TILE, C::PIECES, seen % kRows, lane);
+                if (lane == 0) mbar_arrive(tail_bar);
             }
         } else if (warp == 8) {
             // ----------------------------------------------------- tensor cores
             constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, DP, 0, 1);
-            const auto scores = [&](int x, int slot) {
-                const uint64_t ad = desc_d(sQ + x * C::TILE), bd = desc_d(sKV + slot * C::TILE);
+            const auto scores = [&](int x, int j) {
+                const uint64_t ad = desc_d(sQ + x * C::TILE), bd = desc_d(sK + j % C::KR * C::TILE);
                 const uint32_t dst = tmem + C::TM_S + 128 * x, bar = s_bar(x);
                 if (elect_one()) {
 #pragma unroll
@@ -167,48 +181,50 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
                 }
                 __syncwarp();
             };
-            bool ok = n == 0 || warp_wait(full(0), 0, abort_flag);
-            tc_fence_after();
-            for (int x = 0; x < 2 && ok; ++x)
-                if (tiles[x] > 0) {
-                    ok = warp_wait(q_bar(x), 0, abort_flag);
-                    if (ok) scores(x, 0);
-                }
-            if (ok && n > 0 && elect_one()) mma_commit(empty(0));
-            __syncwarp();
-            for (int j = 0; j < n && ok; ++j) {
-                const int iv = 2 * j + 1, ik = 2 * j + 2;
-                const int sv = iv % C::STAGES, sk = ik % C::STAGES;
-                ok = warp_wait(full(sv), (iv / C::STAGES) & 1, abort_flag);
-                if (ok && j + 1 < n) ok = warp_wait(full(sk), (ik / C::STAGES) & 1, abort_flag);
-                if (!ok) break;
-                if (seen - j * kRows < kRows)
-                    zero_tail(sKV + sv * C::TILE, C::PIECES, seen - j * kRows, lane);
-                for (int x = 0; x < 2 && ok; ++x) {
-                    if (j >= tiles[x]) continue;
-                    ok = warp_wait(p_bar(x), j & 1, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t vd = desc_r(sKV + sv * C::TILE);
+            if (n > 0) warp_wait(k_full(0), 0, abort_flag);
+            if (tiles0 > 0) {
+                warp_wait(q_bar(0), 0, abort_flag);
+                tc_fence_after();
+                scores(0, 0);
+            }
+            if (tiles1 > 0) {
+                warp_wait(q_bar(1), 0, abort_flag);
+                tc_fence_after();
+                scores(1, 0);
+            }
+            for (int j = 0; j < n; ++j) {
+                warp_wait(v_full(j & 1), (j >> 1) & 1, abort_flag);
+                if (j + 1 < n) warp_wait(k_full((j + 1) % C::KR), ((j + 1) / C::KR) & 1, abort_flag);
+                else if (ragged) warp_wait(tail_bar, 0, abort_flag);
+                const uint64_t vd = desc_r(sV + (j & 1) * C::TILE);
+                const uint32_t add = j > 0;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int tiles = x == 0 ? tiles0 : tiles1;
+                    if (j >= tiles) continue;
                     const uint32_t dst = tmem + C::TM_O + DP * x, src = tmem + C::TM_S + 128 * x;
-                    const uint32_t add = j > 0, bar = o_bar(x);
-                    const bool last = j + 1 == tiles[x];
+                    const uint32_t bar = o_bar(x);
+                    const bool last = j + 1 == tiles;
+                    warp_wait(p_bar(x, 0), j & 1, abort_flag);
+                    tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < kRows / 16; ++k)
+                        for (int k = 0; k < 4; ++k)
                             mma_bf16_ta(dst, src + 8 * k, vd + kr(k), id_o, k > 0 ? 1u : add);
+                    }
+                    __syncwarp();
+                    warp_wait(p_bar(x, 1), j & 1, abort_flag);
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 4; k < 8; ++k) mma_bf16_ta(dst, src + 8 * k, vd + kr(k), id_o, 1u);
                         if (last) mma_commit(bar);
                     }
                     __syncwarp();
-                    if (j + 1 < tiles[x]) scores(x, sk);
+                    if (!last) scores(x, j + 1);
                 }
-                if (!ok) break;
-                const uint32_t ev = empty(sv), ek = empty(sk);
-                const bool more = j + 1 < n;
-                if (elect_one()) {
-                    mma_commit(ev);
-                    if (more) mma_commit(ek);
-                }
+                const uint32_t bar = step(j & 1);
+                if (elect_one()) mma_commit(bar);
                 __syncwarp();
             }
             if (elect_one()) mma_commit(done_bar);
@@ -218,20 +234,19 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
         } else {
             // ---------------------------------------------------------- softmax
             const int x = warp >> 2;
-            const int row = threadIdx.x & 127;
-            const int token = first[x] + row / G;  // in its sequence
+            const int row = threadIdx.x & 127, head = row % G;
+            const int first = base + x * tpt, token = first + row / G;  // in the sequence
+            const int tiles = x == 0 ? tiles0 : tiles1;
             const bool valid = row < G * tpt && token < nq;
             const int mine = !valid ? 0 : p.s.causal ? min(nk, token + 1 + nk - nq) : nk;
             // every row of the tile sees the keys before this one
-            const int open = p.s.causal ? first[x] + 1 + nk - nq : nk;
+            const int open = p.s.causal ? first + 1 + nk - nq : nk;
             const float c = p.scale * 1.44269504088896341f;
             const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
             const uint32_t tS = lanes + C::TM_S + 128 * x, tO = lanes + C::TM_O + DP * x;
             float m = -INFINITY, l = 0.f;
-            bool ok = true;
-            for (int j = 0; j < tiles[x]; ++j) {
-                ok = warp_wait(s_bar(x), j & 1, abort_flag);
-                if (!ok) break;
+            for (int j = 0; j < tiles; ++j) {
+                warp_wait(s_bar(x), j & 1, abort_flag);
                 tc_fence_after();
                 float s[128];
 #pragma unroll
@@ -245,8 +260,11 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
                 }
                 float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                for (int i = 4; i < 124; i += 8)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[i + 2 * u], s[i + 2 * u + 1]);
+                const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], s[124], s[125]),
+                                       fmaxf(s[126], s[127]));
                 if (j == 0) {
                     m = top;
                 } else if (__any_sync(~0u, (top - m) * c > 8.f)) {
@@ -255,77 +273,53 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
                     m = mn;
                     l *= keep;
 #pragma unroll 1
-                    for (int q = 0; q < DP; q += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + q, o);
+                    for (int q = 0; q < DP; q += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(tO + q, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
+                        for (int i = 0; i < 16; ++i)
                             o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                        tmem_st32(tO + q, o);
+                        tmem_st16(tO + q, o);
                     }
                 }
                 const float shift = m == -INFINITY ? 0.f : -m * c;
-                float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t w[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float a, d;
-                        fma2(a, d, s[64 * h + 2 * i], s[64 * h + 2 * i + 1], c, shift);
-                        a = exp2_fast(a);
-                        d = exp2_fast(d);
-                        if (i & 1) add2(s0, s1, a, d);
-                        else add2(s2, s3, a, d);
-                        w[i] = pack2(a, d);
+                    for (int q = 64 * h; q < 64 * h + 64; q += 32) {
+                        uint32_t o[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            fma2v(s[q + i], s[q + i + 1], c, shift, shift);
+                            s[q + i] = exp2_fast(s[q + i]);
+                            s[q + i + 1] = exp2_fast(s[q + i + 1]);
+                            o[i / 2] = pack2(s[q + i], s[q + i + 1]);
+                        }
+                        tmem_st16(tS + q / 2, o);
                     }
-                    tmem_st32(tS + 32 * h, w);
+                    tmem_st_wait();
+                    warp_arrive(p_bar(x, h), lane);
+                }
+                float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+                for (int i = 0; i < 128; i += 4) {
+                    add2(s0, s1, s[i], s[i + 1]);
+                    add2(s2, s3, s[i + 2], s[i + 3]);
                 }
                 l += (s0 + s1) + (s2 + s3);
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(p_bar(x));
             }
-            if (ok && tiles[x] > 0) ok = warp_wait(o_bar(x), 0, abort_flag);
-            if (ok && first[x] < nq) {
+            if (tiles > 0) warp_wait(o_bar(x), 0, abort_flag);
+            if (first < nq) {
                 tc_fence_after();
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const long long t = q0 + token;
+                const int h = hk * G + head;
                 if (valid)
-                    p.lse[static_cast<long long>(q0 + token) * p.a.Hq + hk * G + row % G] =
-                        l == 0.f ? -INFINITY : fmaf(m, p.scale, logf(l));
-                // This warp's 32 rows leave through its part of Q_x (all reads of it are
-                // done), 16-byte chunks XORed with the row so that neither side conflicts.
-                constexpr int CH = DP / 8;  // chunks of a row
-                uint8_t* stg = smem_raw + (base - raw) + x * C::TILE + (warp & 3) * 32 * DP * 2;
-#pragma unroll
-                for (int q = 0; q < DP; q += 32) {
-                    uint32_t o[32];
-                    if (tiles[x] > 0) {
-                        tmem_ld32(tO + q, o);
-                        tmem_ld_wait();
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float f[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            f[e] = tiles[x] > 0 && l != 0.f ? __uint_as_float(o[8 * i + e]) * inv : 0.f;
-                        const int ch = (q / 8 + i) ^ (lane & (CH - 1));
-                        *reinterpret_cast<uint4*>(stg + lane * DP * 2 + ch * 16) = pack8(f);
-                    }
-                }
-                __syncwarp();
-                constexpr int RPI = 32 / CH;  // rows a warp writes at once
-#pragma unroll 4
-                for (int i = 0; i < 32; i += RPI) {
-                    const int rl = i + lane / CH, ch = lane % CH;
-                    const int r = (warp & 3) * 32 + rl, t = first[x] + r / G;
-                    if (r < G * tpt && t < nq && ch * 8 < p.a.D)
-                        *reinterpret_cast<uint4*>(p.out.row(q0 + t, hk * G + r % G) + ch * 8) =
-                            *reinterpret_cast<const uint4*>(stg + rl * DP * 2 +
-                                                            (ch ^ (rl & (CH - 1))) * 16);
-                }
+                    p.lse[t * p.a.Hq + h] = l == 0.f ? -INFINITY : fmaf(m, p.scale, logf(l));
+                // The rows leave through Q_x, all reads of which are done.
+                store_rows<DP>(tO, tiles > 0, l == 0.f ? 0.f : 1.f / l,
+                               smem + x * C::TILE + (warp & 3) * 32 * DP * 2, lane,
+                               valid ? p.out.row(t, h) : nullptr, 0, p.a.D);
             }
         }
     }
@@ -353,7 +347,7 @@ cudaError_t forward(const Attention& p, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     LaunchScope ls("attention_forward", st);
-    return launch_k(kfn, dim3(static_cast<unsigned>(items), p.a.Hkv), dim3(kThreads), C::SMEM, st,
+    return launch_k(kfn, dim3(static_cast<unsigned>(items * p.a.Hkv)), dim3(kThreads), C::SMEM, st,
                     mq, mk, mv, prm);
 }
 

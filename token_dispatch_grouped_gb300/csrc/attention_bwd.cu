@@ -15,12 +15,12 @@
 //               product's.
 // Roles as in the forward: a TMA warp, a warp that issues the tcgen05 products, and four
 // groups of four warps that turn scores into weights, each for 32 of the 128 columns of
-// every row (with two groups of 64 columns the tensor cores waited for them: 1.67 and 1.94
-// million cycles a SM for dq and dkv of 8192 tokens, 32/8 heads of 128, against XXX);
-// P and dS go back to TMEM as bf16 operands over the columns that their group has read. The order of the products leaves the tensor cores work while the other warps
-// compute: in dkv_kernel (dP, [P] dV, next S, [dS] dK) P while dP runs and dS while dV and
-// the next S run; in dq_kernel the next S and dP run while dS is formed. TMEM: dq_kernel
-// S, dP twice, dQ; dkv_kernel S, dP, dV, dK (4 x 128 columns).
+// every row; P and dS go back to TMEM as bf16 operands over the columns that their group
+// has read. (Two groups of 64 columns: 652 against 629 us for dq, 697 against 700 for dkv,
+// 8192 tokens, 32/8 heads of 128.) The order of the products leaves the tensor cores work
+// while the other warps compute: in dkv_kernel (dP, [P] dV, next S, [dS] dK) P while dP
+// runs and dS while dV and the next S run; in dq_kernel the next S and dP run while dS is
+// formed. TMEM: dq_kernel S, dP twice, dQ; dkv_kernel S, dP, dV, dK (4 x 128 columns).
 //
 // P and dS are rounded to bf16 (the operand type), everything else is fp32; scale enters
 // dq and dk once at the end. Masked weights are zero by selection, and rows of an operand
@@ -98,24 +98,27 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
     const auto k_full = [&](int s) { return bars + 8u * s; };
     const auto k_empty = [&](int s) { return bars + 8u * (3 + s); };
     const auto v_full = [&](int s) { return bars + 8u * (6 + s); };
-    const auto v_empty = [&](int s) { return bars + 8u * (8 + s); };
     const auto dp_bar = [&](int s) { return bars + 8u * (10 + s); };
     const uint32_t q_bar = bars + 96, do_bar = bars + 104, s_bar = bars + 112,
-                   ds_bar = bars + 120, done_bar = bars + 128, s_read = bars + 136;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 144);
+                   ds_bar = bars + 120, done_bar = bars + 128, s_read = bars + 136,
+                   tail_bar = bars + 144;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 152);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* found = reinterpret_cast<int*>(tmem_slot + 2);
+    Work* found = reinterpret_cast<Work*>(tmem_slot + 2);
     constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DQ = 384;  // dP twice
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 12; ++i) mbar_init(bars + 8 * i, 1);
+        for (int i = 0; i < 8; ++i) mbar_init(bars + 8 * i, 1);
+        mbar_init(dp_bar(0), 1);
+        mbar_init(dp_bar(1), 1);
         mbar_init(q_bar, 1);
         mbar_init(do_bar, 1);
         mbar_init(s_bar, 1);
         mbar_init(ds_bar, kCompute);
         mbar_init(done_bar, 1);
         mbar_init(s_read, kCompute);
+        mbar_init(tail_bar, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -127,29 +130,26 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
     pdl_trigger();
     const int hk = blockIdx.x % p.a.Hkv, tpt = p.tpt, G = p.a.Hq / p.a.Hkv;
     if (warp == 0) {
-        int b = -1, item = 0, items = 0;
         if ((sQ & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
-        const bool skip = __any_sync(~0u, has_error(p.err));
-        if (skip || !find_tile(p.s, false, tpt, blockIdx.x / p.a.Hkv, lane, b, item, items, p.err)) b = -1;
-        if (lane == 0) {
-            found[0] = b;
-            found[1] = items - 1 - item;  // the longest rows of a sequence first
-        }
+        const bool skip = has_error(p.err);
+        Work w = find_work(p.s, false, tpt, blockIdx.x / p.a.Hkv, lane, p.err);
+        if (skip) w.items = 0;
+        if (lane == 0) *found = w;
     }
     if (warp == 1 && blockIdx.x == 0) check_sequences(p.s, lane, p.err);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int b = found[0];
-    if (b >= 0) {
-        const int q0 = p.s.cu_q[b], nq = p.s.cu_q[b + 1] - q0;
-        const int k0 = p.s.cu_k[b], nk = p.s.cu_k[b + 1] - k0;
-        const int first = found[1] * tpt;
+    const Work w = *found;
+    if (w.items > 0) {
+        const int q0 = w.q0, nq = w.nq, k0 = w.k0, nk = w.nk;
+        const int first = (w.items - 1 - w.item) * tpt;  // the longest rows first
         const int seen = p.s.causal ? max(0, min(nk, min(first + tpt, nq) + nk - nq)) : nk;
         const int n = (seen + kRows - 1) / kRows;
 
         if (warp == kCompute + 1) {
+            const bool ragged = seen % kRows != 0;  // the last K tile has rows past the keys
             if (lane == 0 && n > 0) {
                 const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int h, int t) {
                     for (int c = 0; c < C::PIECES; ++c)
@@ -161,8 +161,8 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                 int jk = 0, jv = 0;
                 for (int j = 0; j < n; ++j) {
                     int s = j % C::R0;
-                    if (j >= C::R0 && !wait_phase(k_empty(s), (j / C::R0 - 1) & 1, abort_flag))
-                        break;
+                    if (j >= C::R0) wait_phase(k_empty(s), (j / C::R0 - 1) & 1, abort_flag);
+                    if (*abort_flag) break;
                     mbar_arrive_expect_tx(k_full(s), C::TILE);
                     load(sK + s * C::TILE, &mapK, k_full(s), hk, k0 + j * kRows);
                     ++jk;
@@ -170,27 +170,33 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                         mbar_arrive_expect_tx(do_bar, qbytes);
                         load(sDO, &mapDO, do_bar, hk * G, q0 + first);
                     }
-                    s = j % C::R1;
-                    if (j >= C::R1 && !wait_phase(v_empty(s), (j / C::R1 - 1) & 1, abort_flag))
-                        break;
+                    s = j % C::R1;  // V_{j-2} has been read when dP_{j-2} is there
+                    if (j >= C::R1) wait_phase(dp_bar(s), (j / C::R1 - 1) & 1, abort_flag);
+                    if (*abort_flag) break;
                     mbar_arrive_expect_tx(v_full(s), C::TILE);
                     load(sV + s * C::TILE, &mapV, v_full(s), hk, k0 + j * kRows);
                     ++jv;
                 }
                 // nothing is in flight when the CTA leaves
                 drain(q_bar, 0);
-                drain(do_bar, 0);
+                if (jk > 0) drain(do_bar, 0);
                 for (int j = max(0, jk - C::R0); j < jk; ++j) drain(k_full(j % C::R0), (j / C::R0) & 1);
                 for (int j = max(0, jv - C::R1); j < jv; ++j) drain(v_full(j % C::R1), (j / C::R1) & 1);
             }
+            __syncwarp();
+            if (ragged) {
+                // the last K tile has landed (or the CTA has given up)
+                zero_tail(sK + (n - 1) % C::R0 * C::TILE, C::PIECES, seen % kRows, lane);
+                if (lane == 0) mbar_arrive(tail_bar);
+            }
         } else if (warp == kCompute) {
             constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_q = idesc_bf16(128, DP, 0, 1);
-            // S_j and dP_j, once their keys and values are there
-            const auto scores = [&](int j) -> bool {
+            // S_j and dP_j, once their keys and values are there (rows of K past the keys
+            // zeroed: dQ sums over them)
+            const auto scores = [&](int j) {
                 const int s = j % C::R0;
-                if (!warp_wait(k_full(s), (j / C::R0) & 1, abort_flag)) return false;
-                if (seen - j * kRows < kRows)
-                    zero_tail(sK + s * C::TILE, C::PIECES, seen - j * kRows, lane);
+                warp_wait(k_full(s), (j / C::R0) & 1, abort_flag);
+                if (j + 1 == n && seen % kRows != 0) warp_wait(tail_bar, 0, abort_flag);
                 tc_fence_after();
                 const uint64_t ad = desc_d(sQ), bd = desc_d(sK + s * C::TILE);
                 if (elect_one()) {
@@ -200,33 +206,36 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                     mma_commit(s_bar);
                 }
                 __syncwarp();
-                return true;
             };
-            const auto dprob = [&](int j) -> bool {
+            const auto dprob = [&](int j) {
                 const int s = j % C::R1;
-                if (!warp_wait(v_full(s), (j / C::R1) & 1, abort_flag)) return false;
+                warp_wait(v_full(s), (j / C::R1) & 1, abort_flag);
                 tc_fence_after();
                 const uint64_t ad = desc_d(sDO), bd = desc_d(sV + s * C::TILE);
-                const uint32_t dst = tmem + TM_DP + 128 * (j & 1), bar = dp_bar(j & 1), ve = v_empty(s);
+                const uint32_t dst = tmem + TM_DP + 128 * (j & 1), bar = dp_bar(j & 1);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < DP / 16; ++k) mma_bf16(dst, ad + kd(k), bd + kd(k), id_s, k > 0);
                     mma_commit(bar);
-                    mma_commit(ve);
                 }
                 __syncwarp();
-                return true;
             };
-            bool ok = n == 0 || (warp_wait(q_bar, 0, abort_flag) && scores(0) &&
-                                 warp_wait(do_bar, 0, abort_flag) && dprob(0));
-            for (int j = 0; j < n && ok; ++j) {
+            if (n > 0) {
+                warp_wait(q_bar, 0, abort_flag);
+                scores(0);
+                warp_wait(do_bar, 0, abort_flag);
+                dprob(0);
+            }
+            for (int j = 0; j < n; ++j) {
                 const int sk = j % C::R0;
                 // the next tile's products run while dS_j is formed: S may be overwritten
                 // once it is in registers, and dP has two places
-                if (j + 1 < n)
-                    ok = warp_wait(s_read, j & 1, abort_flag) && scores(j + 1) && dprob(j + 1);
-                ok = ok && warp_wait(ds_bar, j & 1, abort_flag);
-                if (!ok) break;
+                if (j + 1 < n) {
+                    warp_wait(s_read, j & 1, abort_flag);
+                    scores(j + 1);
+                    dprob(j + 1);
+                }
+                warp_wait(ds_bar, j & 1, abort_flag);
                 tc_fence_after();
                 const uint64_t kdesc = desc_r(sK + sk * C::TILE);
                 const uint32_t ke = k_empty(sk), add = j > 0, src = tmem + TM_DP + 128 * (j & 1);
@@ -251,23 +260,34 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
             const int open = p.s.causal ? first + 1 + nk - nq : nk;  // keys that every row sees
             const float c = p.scale * kLog2e;
             const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-            // delta: each group sums a quarter of the row's columns
+            // delta: each group sums its part of the row's columns, all loads at once
             float delta = 0.f, neg_lse = -INFINITY;
-            if (valid) {
-                const bf16* o = p.out.row(q0 + token, hk * G + g);
-                const bf16* d = p.dout.row(q0 + token, hk * G + g);
+            {
+                constexpr int V = DP / kGroups / 8;
+                uint4 o[V], d[V];
+                const bf16* po = p.out.row(q0 + token, hk * G + g);
+                const bf16* pd = p.dout.row(q0 + token, hk * G + g);
 #pragma unroll
-                for (int i = 0; i < DP / kGroups / 8; ++i) {
-                    const int col = grp * (DP / kGroups) + i * 8;
-                    if (col >= p.a.D) break;
+                for (int i = 0; i < V; ++i) {
+                    const int col = (grp * V + i) * 8;
+                    o[i] = d[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (valid && col < p.a.D) {
+                        o[i] = *reinterpret_cast<const uint4*>(po + col);
+                        d[i] = *reinterpret_cast<const uint4*>(pd + col);
+                    }
+                }
+                if (valid) {
+                    const float e = p.lse[static_cast<long long>(q0 + token) * p.a.Hq + hk * G + g];
+                    neg_lse = e == -INFINITY ? e : -e * kLog2e;
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
                     float x[8], y[8];
-                    unpack8(*reinterpret_cast<const uint4*>(o + col), x);
-                    unpack8(*reinterpret_cast<const uint4*>(d + col), y);
+                    unpack8(o[i], x);
+                    unpack8(d[i], y);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) delta += x[e] * y[e];
                 }
-                const float e = p.lse[static_cast<long long>(q0 + token) * p.a.Hq + hk * G + g];
-                neg_lse = e == -INFINITY ? e : -e * kLog2e;
             }
             part_delta[grp * 128 + row] = delta;
             bar_sync(1, kCompute * 32);
@@ -280,10 +300,8 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                 p.row_lse[at] = neg_lse;
                 p.row_delta[at] = neg_delta;
             }
-            bool ok = true;
             for (int j = 0; j < n; ++j) {
-                ok = warp_wait(s_bar, j & 1, abort_flag);
-                if (!ok) break;
+                warp_wait(s_bar, j & 1, abort_flag);
                 tc_fence_after();
                 float s[kCols], d[kCols];
                 load_cols(lanes + TM_S + kCols * grp, s);
@@ -294,8 +312,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                     s[i] = exp2_fast(s[i]);
                     s[i + 1] = exp2_fast(s[i + 1]);
                 }
-                ok = warp_wait(dp_bar(j & 1), (j >> 1) & 1, abort_flag);
-                if (!ok) break;
+                warp_wait(dp_bar(j & 1), (j >> 1) & 1, abort_flag);
                 tc_fence_after();
                 const uint32_t tD = lanes + TM_DP + 128 * (j & 1) + kCols * grp;
                 load_cols(tD, d);
@@ -312,17 +329,12 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                 store_cols(tD, d);
                 warp_arrive(ds_bar, lane);
             }
-            if (ok && n > 0) ok = wait_phase(done_bar, 0, abort_flag);
-            ok = __all_sync(~0u, ok);
-            if (ok) {
+            if (n > 0) warp_wait(done_bar, 0, abort_flag);
+            {
                 tc_fence_after();
                 constexpr int W = DP / kGroups;
-                store_rows<W>(lanes + TM_DQ + grp * W, n > 0, p.scale,
-                              smem + warp * 32 * W * 2, lane, grp * W, p.a.D, [&](int r) -> bf16* {
-                                  const int rr = (warp & 3) * 32 + r, t = first + rr / G;
-                                  return rr < G * tpt && t < nq ? p.dq.row(q0 + t, hk * G + rr % G)
-                                                                : nullptr;
-                              });
+                store_rows<W>(lanes + TM_DQ + grp * W, n > 0, p.scale, smem + warp * 32 * W * 2, lane,
+                              valid ? p.dq.row(q0 + token, hk * G + g) : nullptr, grp * W, p.a.D);
             }
         }
     }
@@ -354,9 +366,10 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
     const uint32_t kv_bar = bars + 96, s_bar = bars + 104, p_bar = bars + 112, dp_bar = bars + 120,
                    ds_bar = bars + 128, done_bar = bars + 136;
     const auto r_empty = [&](int s) { return bars + 144 + 8u * s; };
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 160);
+    const uint32_t tail_bar = bars + 160;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 168);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* found = reinterpret_cast<int*>(tmem_slot + 2);
+    Work* found = reinterpret_cast<Work*>(tmem_slot + 2);
     constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 256 + DP;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -372,6 +385,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
         mbar_init(dp_bar, 1);
         mbar_init(ds_bar, kCompute);
         mbar_init(done_bar, 1);
+        mbar_init(tail_bar, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -379,34 +393,33 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
+    const int hk = blockIdx.x % p.a.Hkv, tpt = p.tpt, G = p.a.Hq / p.a.Hkv;
+    if (G * tpt < kRows && warp < C::R0 + C::R1)  // rows that no load writes: zeros in the sums
+        zero_tail(sQ + warp * C::TILE, C::PIECES, G * tpt, lane);
     pdl_wait();
     pdl_trigger();
-    const int hk = blockIdx.x % p.a.Hkv, tpt = p.tpt, G = p.a.Hq / p.a.Hkv;
     if (warp == 0) {
-        int b = -1, item = 0, items = 0;
         if ((sK & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
-        const bool skip = __any_sync(~0u, has_error(p.err));
-        if (skip || !find_tile(p.s, true, kRows, blockIdx.x / p.a.Hkv, lane, b, item, items, p.err)) b = -1;
-        if (lane == 0) {
-            found[0] = b;
-            found[1] = item;  // the first keys of a sequence are seen most, and come first
-        }
+        const bool skip = has_error(p.err);
+        Work w = find_work(p.s, true, kRows, blockIdx.x / p.a.Hkv, lane, p.err);
+        if (skip) w.items = 0;
+        if (lane == 0) *found = w;
     }
     if (warp == 1 && blockIdx.x == 0) check_sequences(p.s, lane, p.err);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int b = found[0];
-    if (b >= 0) {
-        const int q0 = p.s.cu_q[b], nq = p.s.cu_q[b + 1] - q0;
-        const int k0 = p.s.cu_k[b], nk = p.s.cu_k[b + 1] - k0;
-        const int kv0 = found[1] * kRows;
+    const Work w = *found;
+    if (w.items > 0) {
+        const int q0 = w.q0, nq = w.nq, k0 = w.k0, nk = w.nk;
+        const int kv0 = w.item * kRows;  // the first keys are seen most, and come first
         // query tiles [i0, i0 + n)
         const int i0 = (p.s.causal ? max(0, kv0 - (nk - nq)) : 0) / tpt;
         const int n = max(0, (nq + tpt - 1) / tpt - i0);
         const auto rows_of = [&](int i) { return G * min(tpt, nq - (i0 + i) * tpt); };
 
+        const bool ragged = n > 0 && rows_of(n - 1) < G * tpt;  // the last tile passes the queries
         if (warp == kCompute + 1) {
             if (lane == 0 && n > 0) {
                 const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int h, int t) {
@@ -416,19 +429,19 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
                 const uint32_t qbytes = C::PIECES * 128 * G * tpt;
                 mbar_arrive_expect_tx(kv_bar, 2 * C::TILE);
                 load(sK, &mapK, kv_bar, hk, k0 + kv0);
+                load(sV, &mapV, kv_bar, hk, k0 + kv0);
                 int iq = 0, id = 0;
                 for (int i = 0; i < n; ++i) {
                     const int t = q0 + (i0 + i) * tpt;
                     int s = i % C::R0;
-                    if (i >= C::R0 && !wait_phase(q_empty(s), (i / C::R0 - 1) & 1, abort_flag))
-                        break;
+                    if (i >= C::R0) wait_phase(q_empty(s), (i / C::R0 - 1) & 1, abort_flag);
+                    if (*abort_flag) break;
                     mbar_arrive_expect_tx(q_full(s), qbytes);
                     load(sQ + s * C::TILE, &mapQ, q_full(s), hk * G, t);
                     ++iq;
-                    if (i == 0) load(sV, &mapV, kv_bar, hk, k0 + kv0);
                     s = i % C::R1;
-                    if (i >= C::R1 && !wait_phase(do_empty(s), (i / C::R1 - 1) & 1, abort_flag))
-                        break;
+                    if (i >= C::R1) wait_phase(do_empty(s), (i / C::R1 - 1) & 1, abort_flag);
+                    if (*abort_flag) break;
                     mbar_arrive_expect_tx(do_full(s), qbytes);
                     load(sDO + s * C::TILE, &mapDO, do_full(s), hk * G, t);
                     ++id;
@@ -438,11 +451,18 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
                 for (int i = max(0, iq - C::R0); i < iq; ++i) drain(q_full(i % C::R0), (i / C::R0) & 1);
                 for (int i = max(0, id - C::R1); i < id; ++i) drain(do_full(i % C::R1), (i / C::R1) & 1);
             }
+            __syncwarp();
+            if (ragged) {
+                // the last tiles have landed (or the CTA has given up)
+                zero_tail(sQ + (n - 1) % C::R0 * C::TILE, C::PIECES, rows_of(n - 1), lane);
+                zero_tail(sDO + (n - 1) % C::R1 * C::TILE, C::PIECES, rows_of(n - 1), lane);
+                if (lane == 0) mbar_arrive(tail_bar);
+            }
         } else if (warp == kCompute + 2) {
             // -lse and -delta of each query tile's rows; a row past the sequence or without
             // a key has -lse = -inf (its weights are 0) and delta 0
             for (int i = 0; i < n; ++i) {
-                if (i >= 2 && !warp_wait(r_empty(i & 1), (i / 2 - 1) & 1, abort_flag)) break;
+                if (i >= 2) warp_wait(r_empty(i & 1), (i / 2 - 1) & 1, abort_flag);
                 const int rows = rows_of(i);
                 const long long at =
                     (static_cast<long long>(hk) * p.s.Tq + q0 + (i0 + i) * tpt) * G;
@@ -458,10 +478,10 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
         } else if (warp == kCompute) {
             constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_g = idesc_bf16(128, DP, 0, 1);
             // S^T_i, once its queries are there (rows past them zeroed: dK sums over them)
-            const auto scores = [&](int i) -> bool {
+            const auto scores = [&](int i) {
                 const int s = i % C::R0;
-                if (!warp_wait(q_full(s), (i / C::R0) & 1, abort_flag)) return false;
-                if (rows_of(i) < kRows) zero_tail(sQ + s * C::TILE, C::PIECES, rows_of(i), lane);
+                warp_wait(q_full(s), (i / C::R0) & 1, abort_flag);
+                if (i + 1 == n && ragged) warp_wait(tail_bar, 0, abort_flag);
                 tc_fence_after();
                 const uint64_t ad = desc_d(sK), bd = desc_d(sQ + s * C::TILE);
                 if (elect_one()) {
@@ -471,18 +491,18 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
                     mma_commit(s_bar);
                 }
                 __syncwarp();
-                return true;
             };
-            bool ok = n == 0 || (warp_wait(kv_bar, 0, abort_flag) && scores(0));
-            for (int i = 0; i < n && ok; ++i) {
+            if (n > 0) {
+                warp_wait(kv_bar, 0, abort_flag);
+                scores(0);
+            }
+            for (int i = 0; i < n; ++i) {
                 const int sd = i % C::R1, sq = i % C::R0;
-                ok = warp_wait(do_full(sd), (i / C::R1) & 1, abort_flag);
-                if (!ok) break;
-                if (rows_of(i) < kRows) zero_tail(sDO + sd * C::TILE, C::PIECES, rows_of(i), lane);
-                tc_fence_after();
                 const uint64_t vd = desc_d(sV), dod = desc_d(sDO + sd * C::TILE);
                 const uint64_t dor = desc_r(sDO + sd * C::TILE), qr = desc_r(sQ + sq * C::TILE);
                 const uint32_t de = do_empty(sd), qe = q_empty(sq), add = i > 0;
+                warp_wait(do_full(sd), (i / C::R1) & 1, abort_flag);
+                tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < DP / 16; ++k)
@@ -490,8 +510,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
                     mma_commit(dp_bar);
                 }
                 __syncwarp();
-                ok = warp_wait(p_bar, i & 1, abort_flag);
-                if (!ok) break;
+                warp_wait(p_bar, i & 1, abort_flag);
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -501,9 +520,8 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
                     mma_commit(de);
                 }
                 __syncwarp();
-                if (i + 1 < n) ok = scores(i + 1);
-                ok = ok && warp_wait(ds_bar, i & 1, abort_flag);
-                if (!ok) break;
+                if (i + 1 < n) scores(i + 1);
+                warp_wait(ds_bar, i & 1, abort_flag);
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -523,15 +541,13 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
             const int key = kv0 + row;  // in its sequence
             const float c = p.scale * kLog2e;
             const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-            bool ok = true;
             for (int i = 0; i < n; ++i) {
                 const float* rd = rowdata + (i & 1) * 256 + kCols * grp;
                 // the first token of the tile that sees this key, as the first such column
                 const int from = p.s.causal ? (key - (nk - nq) - (i0 + i) * tpt) * G - kCols * grp : 0;
                 const bool diag = p.s.causal && kv0 + kRows - 1 - (nk - nq) > (i0 + i) * tpt;
-                ok = warp_wait(r_full(i & 1), (i >> 1) & 1, abort_flag) &&
-                     warp_wait(s_bar, i & 1, abort_flag);
-                if (!ok) break;
+                warp_wait(r_full(i & 1), (i >> 1) & 1, abort_flag);
+                warp_wait(s_bar, i & 1, abort_flag);
                 tc_fence_after();
                 float s[kCols], d[kCols];
                 load_cols(lanes + TM_S + kCols * grp, s);
@@ -549,8 +565,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
                 }
                 store_cols(lanes + TM_S + kCols * grp, s);
                 warp_arrive(p_bar, lane);
-                ok = warp_wait(dp_bar, i & 1, abort_flag);
-                if (!ok) break;
+                warp_wait(dp_bar, i & 1, abort_flag);
                 tc_fence_after();
                 load_cols(lanes + TM_DP + kCols * grp, d);
 #pragma unroll
@@ -569,20 +584,16 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
                 warp_arrive(ds_bar, lane);
                 if (lane == 0) mbar_arrive(r_empty(i & 1));
             }
-            if (ok && n > 0) ok = wait_phase(done_bar, 0, abort_flag);
-            ok = __all_sync(~0u, ok);
-            if (ok) {
+            if (n > 0) warp_wait(done_bar, 0, abort_flag);
+            {
                 tc_fence_after();
                 // the first half of the groups: parts of dv; the others: of dk
                 constexpr int PER = kGroups / 2, W = DP / PER;
                 const bool is_v = grp < PER;
-                const Heads& dst = is_v ? p.dv : p.dk;
+                const Heads& to = is_v ? p.dv : p.dk;
                 store_rows<W>(lanes + (is_v ? TM_DV : TM_DK) + (grp % PER) * W, n > 0,
-                              is_v ? 1.f : p.scale, smem + warp * 32 * W * 2, lane, (grp % PER) * W,
-                              p.a.D, [&](int r) -> bf16* {
-                                  const int k = kv0 + (warp & 3) * 32 + r;
-                                  return k < nk ? dst.row(k0 + k, hk) : nullptr;
-                              });
+                              is_v ? 1.f : p.scale, smem + warp * 32 * W * 2, lane,
+                              key < nk ? to.row(k0 + key, hk) : nullptr, (grp % PER) * W, p.a.D);
             }
         }
     }

@@ -156,26 +156,30 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
     if (lane == 0) mbar_arrive(bar);
 }
 
-// Waits for a phase; false when kWaitNs ran out or another role has given up. The roles
+// Waits for a phase, but not longer than kWaitNs or once another role has given up (the
+// abort flag): then every later wait returns after 64 polls at most, the loops run out on
+// whatever their buffers hold, and the CTA reports the time-out. So no role has to agree
+// on a failure with another, and a wait that is already over costs one poll. The roles
 // hand tiles over every few hundred cycles, so the polls are plain try_waits without a
-// suspend hint (a suspended warp woke late), and the clock is read every 64 polls only.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort) {
+// suspend hint (a suspended warp woke late).
+__device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, volatile int* abort) {
+    if (mbar_try_wait(bar, parity)) return;
     uint64_t t0 = 0;
     for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
         if ((i & 63u) != 0) continue;
         const uint64_t t = globaltimer_ns();
         if (t0 == 0) t0 = t;
-        if (*abort) return false;
+        if (*abort) return;
         if (t - t0 > kWaitNs) {
             *abort = 1;
-            return false;
+            return;
         }
     }
-    return true;
 }
-// The same by every lane of a warp, with one answer.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-    return __all_sync(0xffffffffu, wait_phase(bar, parity, abort));
+// The same by a whole warp, which leaves it together.
+__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+    wait_phase(bar, parity, abort);
+    __syncwarp();
 }
 // Bounded wait for something in flight before leaving (given up or not).
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
@@ -184,11 +188,13 @@ __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
         if (globaltimer_ns() - t0 > kWaitNs) break;
 }
 
-// 32 rows x W columns (fp32, TMEM columns t ..) of one warp, times f, as bf16 rows:
-// row(r) gives the row's destination or nullptr. stg: 32 x W x 2 bytes of shared memory.
-template <int W, class Row>
+// 32 rows x W columns (fp32, TMEM columns t ..) of one warp, times f, as bf16 rows. dst:
+// where this lane's row goes (nullptr: nowhere); only columns before D. stg: 32 x W x 2
+// bytes of shared memory, 16-byte chunks XORed with the row so that neither side
+// conflicts.
+template <int W>
 __device__ __forceinline__ void store_rows(uint32_t t, bool any, float f, uint8_t* stg, int lane,
-                                           int col0, int D, Row row) {
+                                           bf16* dst, int col0, int D) {
     constexpr int CH = W / 8;
 #pragma unroll
     for (int q = 0; q < W; q += 16) {
@@ -201,19 +207,22 @@ __device__ __forceinline__ void store_rows(uint32_t t, bool any, float f, uint8_
         for (int i = 0; i < 2; ++i) {
             float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = any && f != 0.f ? __uint_as_float(o[8 * i + e]) * f : 0.f;
+            for (int e = 0; e < 8; ++e)
+                v[e] = any && f != 0.f ? __uint_as_float(o[8 * i + e]) * f : 0.f;
             *reinterpret_cast<uint4*>(stg + lane * W * 2 + ((q / 8 + i) ^ (lane & (CH - 1))) * 16) =
                 pack8(v);
         }
     }
     __syncwarp();
     constexpr int RPI = 32 / CH;
-#pragma unroll 4
+    const unsigned long long at = reinterpret_cast<unsigned long long>(dst);
+    const int ch = lane % CH;
+#pragma unroll
     for (int i = 0; i < 32; i += RPI) {
-        const int rl = i + lane / CH, ch = lane % CH;
-        bf16* dst = row(rl);
-        if (dst != nullptr && col0 + ch * 8 < D)
-            *reinterpret_cast<uint4*>(dst + col0 + ch * 8) =
+        const int rl = i + lane / CH;
+        const unsigned long long to = __shfl_sync(0xffffffffu, at, rl);
+        if (to != 0 && col0 + ch * 8 < D)
+            *reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(to) + col0 + ch * 8) =
                 *reinterpret_cast<const uint4*>(stg + rl * W * 2 + (ch ^ (rl & (CH - 1))) * 16);
     }
 }
@@ -230,18 +239,20 @@ __device__ __forceinline__ void zero_tail(uint32_t tile, int pieces, int first, 
     __syncwarp();
 }
 
-// The sequence and tile of work item `want` when sequence b has ceil(n_b / tile) items,
-// n_b its query (or key) tokens: one warp. Sequences that are not valid have none.
-// Returns false past the last item.
-__device__ __forceinline__ bool find_tile(const Packed& s, bool keys, int tile, int want, int lane,
-                                          int& b, int& item, int& items, int* err) {
+// A CTA's part of the batch: tokens of its sequence and the tile of them that it works on.
+struct Work {
+    int q0, nq, k0, nk;
+    int item, items;  // items 0: nothing to do
+};
+// Work item `want` when a sequence has ceil(n / tile) items, n its query (or key) tokens:
+// one warp. Sequences that are not valid have none.
+__device__ __forceinline__ Work find_work(const Packed& s, bool keys, int tile, int want, int lane,
+                                          int* err) {
     int before = 0;
     for (int b0 = 0; b0 < s.B; b0 += 32) {
-        int n = 0;
-        if (b0 + lane < s.B) {
-            int q0, nq, k0, nk;
-            if (sequence_of(s, b0 + lane, q0, nq, k0, nk, err)) n = ((keys ? nk : nq) + tile - 1) / tile;
-        }
+        int n = 0, q0 = 0, nq = 0, k0 = 0, nk = 0;
+        if (b0 + lane < s.B && sequence_of(s, b0 + lane, q0, nq, k0, nk, err))
+            n = ((keys ? nk : nq) + tile - 1) / tile;
         int incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -251,15 +262,18 @@ __device__ __forceinline__ bool find_tile(const Packed& s, bool keys, int tile, 
         const uint32_t past = __ballot_sync(0xffffffffu, want < before + incl);
         if (past) {
             const int l = __ffs(past) - 1;
-            const int end = __shfl_sync(0xffffffffu, incl, l);
-            items = __shfl_sync(0xffffffffu, n, l);
-            item = want - (before + end - items);
-            b = b0 + l;
-            return true;
+            Work w;
+            w.q0 = __shfl_sync(0xffffffffu, q0, l);
+            w.nq = __shfl_sync(0xffffffffu, nq, l);
+            w.k0 = __shfl_sync(0xffffffffu, k0, l);
+            w.nk = __shfl_sync(0xffffffffu, nk, l);
+            w.items = __shfl_sync(0xffffffffu, n, l);
+            w.item = want - (before + __shfl_sync(0xffffffffu, incl, l) - w.items);
+            return w;
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
     }
-    return false;
+    return {0, 0, 0, 0, 0, 0};
 }
 // Upper bound of the items, known on the host.
 inline long long tile_bound(int T, int B, int longest, int tile) {

@@ -129,7 +129,8 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
         int i = 0;
         for (; i < stages; ++i) {
             const int slot = i % C::STAGES;
-            if (i >= C::STAGES && !warp_wait(empty(slot), (i / C::STAGES - 1) & 1, abort_flag)) break;
+            if (i >= C::STAGES) warp_wait(empty(slot), (i / C::STAGES - 1) & 1, abort_flag);
+            if (__any_sync(~0u, *abort_flag != 0)) break;
             // box x of this stage: rows x * rows .. of K and V; lane x has its page
             const int tok = t0 + i * kTokens + lane * rows;
             const bool mine = lane < kTokens / rows && tok < t1;
@@ -182,12 +183,10 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
         float o[DP / 8][4];
 #pragma unroll
         for (int d = 0; d < DP / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
-        bool ok = true;
         for (int i = 0; i < stages; ++i) {
             const int slot = i % C::STAGES;
             const int tok = t0 + i * kTokens + 16 * warp;  // this warp's first token
-            ok = warp_wait(full(slot), (i / C::STAGES) & 1, abort_flag);
-            if (!ok) break;
+            warp_wait(full(slot), (i / C::STAGES) & 1, abort_flag);
             if (tok < t1) {
                 const uint32_t sK = base + slot * C::STAGE, sV = sK + C::HALF;
                 float s[2][4] = {};
