@@ -44,7 +44,7 @@ int check_rope(const moe_attn_shape& a, const moe_rope& r, const int32_t* positi
     if (r.dims < 0 || r.dims % 2 != 0 || r.dims > a.D || r.positions < 1 || !r.table ||
         !positions || (r.layout != MOE_ROPE_HALF && r.layout != MOE_ROPE_INTERLEAVED))
         return MOE_ERR_INVALID_ARG;
-    if (reinterpret_cast<uintptr_t>(r.table) & 7u) return MOE_ERR_MISALIGNED;
+    if (!aligned16(r.table)) return MOE_ERR_MISALIGNED;
     return MOE_OK;
 }
 

@@ -9,13 +9,16 @@
 // Backward: dy is the upstream gradient rotated by -p, and with n = x r:
 //   dx = r (dy w - n mean(dy w n)),   dw = sum over rows of dy n.
 //
-// Both directions are bound by memory (2 or 3 x 2 bytes a value, a few flops each).
-// A head row is read as 16-byte pieces of 8 values, so D / 8 lanes (8 or 16 with
-// padding) hold one row and a warp holds 2 to 4 rows at once. A lane keeps the same
-// piece of every head of a token, so it reads its (cos, sin) once per token and keeps
-// them in registers over the token's heads. Pairs of the half layout lie in another
-// lane's registers: a shuffle fetches them when dims / 2 is a multiple of 8 (whole
-// pieces swap), else the row passes through shared memory.
+// Both directions are bound by memory (2 or 3 x 2 bytes a value), if their instructions
+// are few: a head row is read as 16-byte pieces of 8 values, so D / 8 lanes (8 or 16 with
+// padding) hold one row and a warp holds 2 to 4 rows at once. A warp takes rows of one
+// kind (queries, keys or values) of one token, so what they share is formed once, in
+// registers: out_i = r (x_i A_i + x_{partner(i)} B_i) with A = w cos, B = w_{partner} sin'.
+// The partner's values are exchanged as they were read, two bf16 a register: from the
+// lane's own registers (interleaved), by shuffles (half layout, when whole pieces swap), or
+// through shared memory (any other number of rotated dims). Arithmetic is two fp32
+// operations an instruction. (One weight load and one fp32 shuffle a value, at half the
+// warps: 34.8 us for 4096 tokens of 32/8 heads of 128 against XXX.)
 #include "attn.cuh"
 
 namespace moe {
@@ -24,72 +27,104 @@ namespace {
 
 constexpr int kWarps = 8;
 
-// Where a lane's rotated partners are: none (no rotation), in its own registers
-// (interleaved), in another lane (half layout, whole pieces) or anywhere in the row.
 enum Swap { SWAP_NONE = 0, SWAP_OWN = 1, SWAP_LANE = 2, SWAP_ROW = 3 };
 
 Swap swap_of(const NormRope& p) {
     if (p.rot == 0) return SWAP_NONE;
-    if (p.interleaved) return SWAP_OWN;
-    return (p.rot / 2) % 8 == 0 ? SWAP_LANE : SWAP_ROW;
+    if (p.interleaved) return p.rot % 8 == 0 ? SWAP_OWN : SWAP_ROW;
+    return p.rot % 16 == 0 ? SWAP_LANE : SWAP_ROW;
 }
 
-// A lane's rotation factors of one token.
+// The other value of i's pair.
+__device__ __forceinline__ int partner_of(int i, int rot, int interleaved) {
+    if (i >= rot) return i;
+    if (interleaved) return i ^ 1;
+    const int half = rot >> 1;
+    return i < half ? i + half : i - half;
+}
+
+// cos and sin' of a lane's piece at one position (1 and 0 past the rotated dims).
 template <int SWAP>
-struct Rotation {
-    float c[8], s[8];
-    // piece: first value / 8; dir: +1 rotates by the position, -1 back.
-    __device__ __forceinline__ void load(const float2* row, int rot, int piece, float dir) {
-        if constexpr (SWAP == SWAP_NONE) return;
+__device__ __forceinline__ void load_rotation(const float2* row, int rot, int interleaved, int piece,
+                                              float (&c)[8], float (&s)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        c[e] = 1.f;
+        s[e] = 0.f;
+    }
+    if constexpr (SWAP == SWAP_OWN) {
+        if (piece * 8 < rot) {
+            const float4* t = reinterpret_cast<const float4*>(row + piece * 4);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float4 v = __ldg(t + u);
+                c[4 * u] = c[4 * u + 1] = v.x;
+                s[4 * u] = -v.y;
+                s[4 * u + 1] = v.y;
+                c[4 * u + 2] = c[4 * u + 3] = v.z;
+                s[4 * u + 2] = -v.w;
+                s[4 * u + 3] = v.w;
+            }
+        }
+    } else if constexpr (SWAP == SWAP_LANE) {
+        const int hop = rot >> 4;  // pieces in half of the rotated dims
+        if (piece < 2 * hop) {
+            const bool lo = piece < hop;
+            const float4* t = reinterpret_cast<const float4*>(row + (lo ? piece : piece - hop) * 8);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float4 v = __ldg(t + u);
+                c[2 * u] = v.x;
+                s[2 * u] = lo ? -v.y : v.y;
+                c[2 * u + 1] = v.z;
+                s[2 * u + 1] = lo ? -v.w : v.w;
+            }
+        }
+    } else if constexpr (SWAP == SWAP_ROW) {
         const int half = rot >> 1;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int i = piece * 8 + e;
-            int at;
-            float sign;
-            if constexpr (SWAP == SWAP_OWN) {
-                at = i >> 1;
-                sign = (e & 1) ? dir : -dir;
-            } else {
-                at = i < half ? i : i - half;
-                sign = i < half ? -dir : dir;
-            }
-            const float2 cs = i < rot ? __ldg(row + at) : make_float2(1.f, 0.f);
-            c[e] = cs.x;
-            s[e] = sign * cs.y;
+            if (i >= rot) continue;
+            const float2 v = __ldg(row + (interleaved ? i >> 1 : i < half ? i : i - half));
+            const bool firstv = interleaved ? (i & 1) == 0 : i < half;
+            c[e] = v.x;
+            s[e] = firstv ? -v.y : v.y;
         }
     }
-    // buf: this row's 128 floats of shared memory (SWAP_ROW); every lane of the warp
-    // calls this.
-    template <int LPR>
-    __device__ __forceinline__ void apply(float (&y)[8], int rot, int piece, float* buf) const {
-        if constexpr (SWAP == SWAP_NONE) return;
-        float o[8];
-        if constexpr (SWAP == SWAP_OWN) {
+}
+
+// The partners of a lane's 8 values (0 past the rotated dims, where they have no part).
+// buf: this row's 128 bf16 of shared memory (SWAP_ROW). Every lane of the warp calls this.
+template <int LPR, int SWAP>
+__device__ __forceinline__ void partners(const uint4& in, const float (&x)[8], int rot,
+                                         int interleaved, int piece, bf16* buf, float (&o)[8]) {
+    if constexpr (SWAP == SWAP_OWN) {
+        const bool on = piece * 8 < rot;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = y[e ^ 1];
-        } else if constexpr (SWAP == SWAP_LANE) {
-            const int hop = rot >> 4;  // pieces in half of the rotated dims
-            const int from = piece < hop ? piece + hop : piece < 2 * hop ? piece - hop : piece;
+        for (int e = 0; e < 8; ++e) o[e] = on ? x[e ^ 1] : 0.f;
+    } else if constexpr (SWAP == SWAP_LANE) {
+        const int hop = rot >> 4;
+        const bool on = piece < 2 * hop;
+        const int from = !on ? piece : piece < hop ? piece + hop : piece - hop;
+        uint4 v;
+        v.x = __shfl_sync(0xffffffffu, in.x, from, LPR);
+        v.y = __shfl_sync(0xffffffffu, in.y, from, LPR);
+        v.z = __shfl_sync(0xffffffffu, in.z, from, LPR);
+        v.w = __shfl_sync(0xffffffffu, in.w, from, LPR);
+        if (!on) v = make_uint4(0u, 0u, 0u, 0u);
+        unpack8(v, o);
+    } else if constexpr (SWAP == SWAP_ROW) {
+        __syncwarp();
+        *reinterpret_cast<uint4*>(buf + piece * 8) = in;
+        __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xffffffffu, y[e], from, LPR);
-        } else {
-            const int half = rot >> 1;
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) buf[piece * 8 + e] = y[e];
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int i = piece * 8 + e;
-                o[e] = buf[i < half ? i + half : i < rot ? i - half : i];
-            }
+        for (int e = 0; e < 8; ++e) {
+            const int i = piece * 8 + e;
+            o[e] = i < rot ? __bfloat162float(buf[partner_of(i, rot, interleaved)]) : 0.f;
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (piece * 8 + e < rot) y[e] = y[e] * c[e] + o[e] * s[e];
     }
-};
+}
 
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v) {
@@ -98,205 +133,257 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// One warp per (token, run of its rows): rows 0 .. Hq are queries, then Hkv keys, then
-// (append) Hkv values, which are only copied.
+// Which rows of which token a warp takes: a token has q runs of its queries, k of its keys
+// and v of its values (append), of at most `rows` rows.
+struct Runs {
+    int q, k, v, rows;
+    int total() const { return q + k + v; }
+};
+
 template <int LPR, int SWAP, bool APPEND>
-__global__ void __launch_bounds__(kWarps * 32)
-norm_rope_kernel(const NormRope p, int runs, int run_rows) {
+__global__ void __launch_bounds__(kWarps * 32, 3)
+norm_rope_kernel(const NormRope p, const Runs rn, int runs) {
     constexpr int RPW = 32 / LPR;  // rows of a warp at once
     constexpr int U = 4;           // loads in flight per lane
-    __shared__ float s_buf[SWAP == SWAP_ROW ? kWarps * RPW * 128 : 1];
+    __shared__ __align__(16) bf16 s_buf[SWAP == SWAP_ROW ? kWarps * RPW * 128 : 8];
     pdl_wait();
     pdl_trigger();
-    if (has_error(p.err)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long task = static_cast<long long>(blockIdx.x) * kWarps + warp;
     const int t = static_cast<int>(task / runs);
-    if (t >= p.T) return;
+    if (t >= p.T || has_error(p.err)) return;
+    int run = static_cast<int>(task % runs), kind = 0;  // 0 queries, 1 keys, 2 values
+    if (run >= rn.q) {
+        run -= rn.q;
+        kind = 1;
+        if (APPEND && run >= rn.k) {
+            run -= rn.k;
+            kind = 2;
+        }
+    }
     const int piece = lane % LPR, sub = lane / LPR;
-    const int D = p.a.D, Hq = p.a.Hq, Hkv = p.a.Hkv;
-    const int rows = Hq + (p.k.p ? Hkv : 0) + (APPEND ? Hkv : 0);
-    const int r0 = static_cast<int>(task % runs) * run_rows, r1 = min(rows, r0 + run_rows);
+    const int D = p.a.D, Hkv = p.a.Hkv;
+    const int r0 = run * rn.rows, r1 = min(kind == 0 ? p.a.Hq : Hkv, r0 + rn.rows);
     const bool live = piece * 8 < D;
+    const Heads src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+    const bf16* in_row = src.row(t, r0 + sub) + piece * 8;
 
-    long long cache_row = -1;  // (page * Hkv) * page_size + row of the page, head 0
-    if constexpr (APPEND) {
-        const long long slot = p.slots[t];
-        if (slot >= (static_cast<long long>(p.pages) << p.page_shift)) {
-            if (lane == 0) raise_error(p.err, MOE_ERR_BAD_INDEX);
-        } else if (slot >= 0) {
-            const long long page = slot >> p.page_shift;
-            cache_row = ((page * Hkv) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
-        }
-    }
-    Rotation<SWAP> rot;
-    bool bad = false;
-    if constexpr (SWAP != SWAP_NONE) {
-        const int pos = p.positions[t];
-        bad = pos < 0 || pos >= p.table_rows;
-        if (bad) {
-            if (lane == 0) raise_error(p.err, MOE_ERR_BAD_INDEX);
-        } else {
-            rot.load(p.table + static_cast<long long>(pos) * (p.rot >> 1), p.rot, piece, 1.f);
-        }
-    }
-    if (bad) return;  // the whole warp: one token
-    const bool norm = p.wq != nullptr;
-    float* buf = s_buf + (SWAP == SWAP_ROW ? (warp * RPW + sub) * 128 : 0);
-
-    for (int rb = r0; rb < r1; rb += RPW * U) {
-        uint4 in[U];
+    uint4 in[U];
+    const auto load = [&](int rb) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = rb + u * RPW + sub;
-            in[u] = make_uint4(0, 0, 0, 0);
-            if (r < r1 && live) {
-                const bf16* src = r < Hq ? p.q.row(t, r)
-                                  : !APPEND || r < Hq + Hkv ? p.k.row(t, r - Hq)
-                                                            : p.v.row(t, r - Hq - Hkv);
-                in[u] = *reinterpret_cast<const uint4*>(src + piece * 8);
+            in[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (rb + u * RPW + sub < r1 && live)
+                in[u] = *reinterpret_cast<const uint4*>(in_row + (rb - r0 + u * RPW) * src.hs);
+        }
+    };
+    load(r0);
+
+    // where the rows go
+    bf16* out = (kind == 0 ? p.q_out : p.k_out).row(t, r0 + sub) + piece * 8;
+    long long out_hs = (kind == 0 ? p.q_out : p.k_out).hs;
+    if constexpr (APPEND) {
+        if (kind > 0) {
+            const long long slot = p.slots[t];
+            if (slot >= (static_cast<long long>(p.pages) << p.page_shift)) {
+                if (lane == 0) raise_error(p.err, MOE_ERR_BAD_INDEX);
+                return;
+            }
+            if (slot < 0) return;
+            const long long page = slot >> p.page_shift;
+            out_hs = static_cast<long long>(D) << p.page_shift;
+            out = (kind == 1 ? p.k_pages : p.v_pages) + (page * Hkv + r0 + sub) * out_hs +
+                  (slot & ((1 << p.page_shift) - 1)) * D + piece * 8;
+        }
+        if (kind == 2) {
+            for (int rb = r0; rb < r1; rb += RPW * U) {
+                if (rb > r0) load(rb);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (rb + u * RPW + sub < r1 && live)
+                        *reinterpret_cast<uint4*>(out + (rb - r0 + u * RPW) * out_hs) = in[u];
+            }
+            return;
+        }
+    }
+    const bool norm = p.wq != nullptr;
+    float a[8], b[8];  // A and B
+    if constexpr (SWAP != SWAP_NONE) {
+        const int pos = p.positions[t];
+        if (pos < 0 || pos >= p.table_rows) {  // the whole warp: one token
+            if (lane == 0) raise_error(p.err, MOE_ERR_BAD_INDEX);
+            return;
+        }
+        load_rotation<SWAP>(p.table + static_cast<long long>(pos) * (p.rot >> 1), p.rot,
+                            p.interleaved, piece, a, b);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] = 1.f;
+    }
+    if (norm && live) {
+        const float* w = kind == 0 ? p.wq : p.wk;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            a[e] *= __ldg(w + piece * 8 + e);
+            if constexpr (SWAP != SWAP_NONE) {
+                int at = piece * 8 + e;
+                if constexpr (SWAP == SWAP_OWN) at = piece * 8 < p.rot ? at ^ 1 : at;
+                else at = partner_of(at, p.rot, p.interleaved);
+                b[e] *= __ldg(w + at);
             }
         }
+    }
+    bf16* buf = s_buf + (SWAP == SWAP_ROW ? (warp * RPW + sub) * 128 : 0);
+    const float inv_d = 1.f / static_cast<float>(D);
+
+    for (int rb = r0; rb < r1; rb += RPW * U) {
+        if (rb > r0) load(rb);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (rb + u * RPW >= r1) break;  // the same for the whole warp
-            const int r = rb + u * RPW + sub;
-            float y[8];
-            unpack8(in[u], y);
-            float ss = 0.f;
+            float x[8], y[8];
+            unpack8(in[u], x);
+            float rr = 1.f;
+            if (norm) {
+                float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss += y[e] * y[e];
-            ss = row_sum<LPR>(ss);
-            if (norm && live) {
-                const float rr = rsqrtf(ss / static_cast<float>(D) + p.eps);
-                const float4* w = reinterpret_cast<const float4*>((r < Hq ? p.wq : p.wk) + piece * 8);
-                const float4 w0 = __ldg(w), w1 = __ldg(w + 1);
-                const float wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                for (int e = 0; e < 8; e += 2) fma2(s0, s1, x[e], x[e + 1], x[e], x[e + 1]);
+                rr = rsqrtf(row_sum<LPR>(s0 + s1) * inv_d + p.eps);
+            }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = y[e] * rr * wv[e];
+            for (int e = 0; e < 8; ++e) y[e] = x[e];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) mul2(y[e], y[e + 1], a[e], a[e + 1]);
+            if constexpr (SWAP != SWAP_NONE) {
+                float o[8];
+                partners<LPR, SWAP>(in[u], x, p.rot, p.interleaved, piece, buf, o);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) fma2(y[e], y[e + 1], o[e], o[e + 1], b[e], b[e + 1]);
             }
-            rot.template apply<LPR>(y, p.rot, piece, buf);
-            if (r >= r1 || !live) continue;
-            if (r < Hq) {
-                *reinterpret_cast<uint4*>(p.q_out.row(t, r) + piece * 8) = pack8(y);
-            } else if constexpr (APPEND) {
-                if (cache_row < 0) continue;
-                const bool key = r < Hq + Hkv;
-                const int h = r - Hq - (key ? 0 : Hkv);
-                const long long at = (cache_row + (static_cast<long long>(h) << p.page_shift)) * D;
-                *reinterpret_cast<uint4*>((key ? p.k_pages : p.v_pages) + at + piece * 8) =
-                    key ? pack8(y) : in[u];
-            } else {
-                *reinterpret_cast<uint4*>(p.k_out.row(t, r - Hq) + piece * 8) = pack8(y);
-            }
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) mul2(y[e], y[e + 1], rr, rr);
+            if (rb + u * RPW + sub < r1 && live)
+                *reinterpret_cast<uint4*>(out + (rb - r0 + u * RPW) * out_hs) = pack8(y);
         }
     }
 }
 
-// Backward: warps walk the (token, run) tasks with the grid's stride and keep their
-// piece of the two weight gradients in registers; a CTA adds its warps' sums in warp
-// order and writes one partial row [2][D].
+// Backward: with the upstream gradient g rotated back, dy_i = g_i cos_i - g_partner sin'_i,
+// and q = sum dy w x: dx = r dy w - x r^3 q / D, dw += r dy x. A warp walks (token, run)
+// tasks of the queries, then of the keys, with the grid's stride, and keeps its piece of
+// that weight gradient in registers; a CTA adds its warps' sums in warp order and writes
+// one partial row [2][D].
 template <int LPR, int SWAP>
-__global__ void __launch_bounds__(kWarps * 32)
-norm_rope_backward_kernel(const NormRope p, Heads dq_out, Heads dk_out, float* part, int runs,
-                          int run_rows) {
+__global__ void __launch_bounds__(kWarps * 32, 2)
+norm_rope_backward_kernel(const NormRope p, Heads dq_out, Heads dk_out, float* part, const Runs rn) {
     constexpr int RPW = 32 / LPR;
-    constexpr int U = 2;  // two rows' x and dout in flight per lane
-    __shared__ float s_buf[SWAP == SWAP_ROW ? kWarps * RPW * 128 : 1];
+    constexpr int U = 2;  // two rows' x and g in flight per lane
+    __shared__ __align__(16) bf16 s_buf[SWAP == SWAP_ROW ? kWarps * RPW * 128 : 8];
     __shared__ float s_dw[kWarps][2][128];
     pdl_wait();
     pdl_trigger();
     if (has_error(p.err)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int piece = lane % LPR, sub = lane / LPR;
-    const int D = p.a.D, Hq = p.a.Hq;
-    const int rows = Hq + (p.k.p ? p.a.Hkv : 0);
+    const int D = p.a.D;
     const bool live = piece * 8 < D;
     const bool norm = p.wq != nullptr;
-    float* buf = s_buf + (SWAP == SWAP_ROW ? (warp * RPW + sub) * 128 : 0);
-    float aq[8], ak[8], wq[8], wk[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        aq[e] = ak[e] = 0.f;
-        wq[e] = norm && live ? p.wq[piece * 8 + e] : 1.f;
-        wk[e] = norm && live ? p.wk[piece * 8 + e] : 1.f;
-    }
-    const long long tasks = static_cast<long long>(p.T) * runs;
+    bf16* buf = s_buf + (SWAP == SWAP_ROW ? (warp * RPW + sub) * 128 : 0);
+    const float inv_d = 1.f / static_cast<float>(D);
     const long long step = static_cast<long long>(gridDim.x) * kWarps;
-    for (long long task = static_cast<long long>(blockIdx.x) * kWarps + warp; task < tasks;
-         task += step) {
-        const int t = static_cast<int>(task / runs);
-        const int r0 = static_cast<int>(task % runs) * run_rows, r1 = min(rows, r0 + run_rows);
-        Rotation<SWAP> rot;
-        if constexpr (SWAP != SWAP_NONE) {
-            const int pos = p.positions[t];
-            if (pos < 0 || pos >= p.table_rows) {
-                if (lane == 0) raise_error(p.err, MOE_ERR_BAD_INDEX);
-                continue;
-            }
-            rot.load(p.table + static_cast<long long>(pos) * (p.rot >> 1), p.rot, piece, -1.f);
+#pragma unroll 1
+    for (int kind = 0; kind < 2; ++kind) {
+        float acc[8], w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            acc[e] = 0.f;
+            w[e] = norm && live ? (kind == 0 ? p.wq : p.wk)[piece * 8 + e] : 1.f;
         }
-        for (int rb = r0; rb < r1; rb += RPW * U) {
+        const Heads xs = kind == 0 ? p.q : p.k, gs = kind == 0 ? dq_out : dk_out;
+        const Heads os = kind == 0 ? p.q_out : p.k_out;
+        const int runs = kind == 0 ? rn.q : rn.k, rows = kind == 0 ? p.a.Hq : p.a.Hkv;
+        const long long tasks = static_cast<long long>(p.T) * runs;
+        for (long long task = static_cast<long long>(blockIdx.x) * kWarps + warp; task < tasks;
+             task += step) {
+            const int t = static_cast<int>(task / runs);
+            const int r0 = static_cast<int>(task % runs) * rn.rows, r1 = min(rows, r0 + rn.rows);
+            const bf16* xr = xs.row(t, r0 + sub) + piece * 8;
+            const bf16* gr = gs.row(t, r0 + sub) + piece * 8;
+            bf16* orow = os.row(t, r0 + sub) + piece * 8;
             uint4 xin[U], gin[U];
+            const auto load = [&](int rb) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int r = rb + u * RPW + sub;
-                xin[u] = gin[u] = make_uint4(0, 0, 0, 0);
-                if (r < r1 && live) {
-                    const bf16* x = r < Hq ? p.q.row(t, r) : p.k.row(t, r - Hq);
-                    const bf16* g = r < Hq ? dq_out.row(t, r) : dk_out.row(t, r - Hq);
-                    xin[u] = *reinterpret_cast<const uint4*>(x + piece * 8);
-                    gin[u] = *reinterpret_cast<const uint4*>(g + piece * 8);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (rb + u * RPW >= r1) break;  // the same for the whole warp
-                const int r = rb + u * RPW + sub;
-                const bool isq = r < Hq;
-                float x[8], dy[8];
-                unpack8(xin[u], x);
-                unpack8(gin[u], dy);
-                rot.template apply<LPR>(dy, p.rot, piece, buf);
-                if (norm) {
-                    float ss = 0.f, sd = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        ss += x[e] * x[e];
-                        sd += dy[e] * (isq ? wq[e] : wk[e]) * x[e];
-                    }
-                    ss = row_sum<LPR>(ss);
-                    sd = row_sum<LPR>(sd);
-                    const float rr = rsqrtf(ss / static_cast<float>(D) + p.eps);
-                    const float m = sd * rr / static_cast<float>(D);  // mean(dy w n)
-                    const bool mine = r < r1 && live;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float n = x[e] * rr;
-                        if (mine && isq) aq[e] += dy[e] * n;
-                        if (mine && !isq) ak[e] += dy[e] * n;
-                        dy[e] = rr * (dy[e] * (isq ? wq[e] : wk[e]) - n * m);
+                for (int u = 0; u < U; ++u) {
+                    xin[u] = gin[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (rb + u * RPW + sub < r1 && live) {
+                        xin[u] = *reinterpret_cast<const uint4*>(xr + (rb - r0 + u * RPW) * xs.hs);
+                        gin[u] = *reinterpret_cast<const uint4*>(gr + (rb - r0 + u * RPW) * gs.hs);
                     }
                 }
-                if (r < r1 && live)
-                    *reinterpret_cast<uint4*>((isq ? p.q_out.row(t, r) : p.k_out.row(t, r - Hq)) +
-                                              piece * 8) = pack8(dy);
+            };
+            load(r0);
+            float c[8], s[8];
+            if constexpr (SWAP != SWAP_NONE) {
+                const int pos = p.positions[t];
+                if (pos < 0 || pos >= p.table_rows) {
+                    if (lane == 0) raise_error(p.err, MOE_ERR_BAD_INDEX);
+                    continue;
+                }
+                load_rotation<SWAP>(p.table + static_cast<long long>(pos) * (p.rot >> 1), p.rot,
+                                    p.interleaved, piece, c, s);
             }
+            for (int rb = r0; rb < r1; rb += RPW * U) {
+                if (rb > r0) load(rb);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (rb + u * RPW >= r1) break;  // the same for the whole warp
+                    float x[8], dy[8];
+                    unpack8(xin[u], x);
+                    unpack8(gin[u], dy);
+                    if constexpr (SWAP != SWAP_NONE) {
+                        float o[8];
+                        partners<LPR, SWAP>(gin[u], dy, p.rot, p.interleaved, piece, buf, o);
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) {
+                            mul2(dy[e], dy[e + 1], c[e], c[e + 1]);
+                            fma2(dy[e], dy[e + 1], o[e], o[e + 1], -s[e], -s[e + 1]);
+                        }
+                    }
+                    if (norm) {
+                        float s0 = 0.f, s1 = 0.f, q0 = 0.f, q1 = 0.f, g[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) {
+                            fma2(s0, s1, x[e], x[e + 1], x[e], x[e + 1]);
+                            g[e] = dy[e];
+                            g[e + 1] = dy[e + 1];
+                            mul2(g[e], g[e + 1], x[e], x[e + 1]);           // dy x
+                            fma2(q0, q1, g[e], g[e + 1], w[e], w[e + 1]);
+                        }
+                        // rows past the run are zeros and add nothing
+                        float rr = rsqrtf(row_sum<LPR>(s0 + s1) * inv_d + p.eps);
+                        if (rb + u * RPW + sub >= r1) rr = 0.f;
+                        const float k = -rr * rr * rr * (row_sum<LPR>(q0 + q1) * inv_d);
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) {
+                            fma2(acc[e], acc[e + 1], g[e], g[e + 1], rr, rr);
+                            mul2(dy[e], dy[e + 1], w[e], w[e + 1]);
+                            mul2(dy[e], dy[e + 1], rr, rr);
+                            fma2(dy[e], dy[e + 1], x[e], x[e + 1], k, k);
+                        }
+                    }
+                    if (rb + u * RPW + sub < r1 && live)
+                        *reinterpret_cast<uint4*>(orow + (rb - r0 + u * RPW) * os.hs) = pack8(dy);
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+#pragma unroll
+            for (int o = LPR; o < 32; o <<= 1) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
+            if (sub == 0 && live) s_dw[warp][kind][piece * 8 + e] = acc[e];
         }
     }
     if (!norm) return;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-#pragma unroll
-        for (int o = LPR; o < 32; o <<= 1) {
-            aq[e] += __shfl_xor_sync(0xffffffffu, aq[e], o);
-            ak[e] += __shfl_xor_sync(0xffffffffu, ak[e], o);
-        }
-        if (sub == 0 && live) {
-            s_dw[warp][0][piece * 8 + e] = aq[e];
-            s_dw[warp][1][piece * 8 + e] = ak[e];
-        }
-    }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {
         const int which = i / D, col = i % D;
@@ -308,7 +395,7 @@ norm_rope_backward_kernel(const NormRope p, Heads dq_out, Heads dk_out, float* p
 }
 
 // dw[col] = sum of the partial rows: 32 threads a column take every 32nd row, then add
-// in thread order pairs (a fixed tree).
+// in a fixed tree.
 __global__ void __launch_bounds__(1024)
 norm_rope_dw_kernel(const float* part, int parts, int D, float* dwq, float* dwk, int* err) {
     __shared__ float s[32][33];
@@ -344,40 +431,37 @@ __global__ void rope_table_kernel(long long n, int half, const double* inv_freq,
     table[i] = make_float2(static_cast<float>(scale * c), static_cast<float>(scale * s));
 }
 
-// How a token's rows are cut into runs (one warp each): whole tokens when there are
-// enough of them to fill the GPU, else pieces down to the rows a warp holds at once.
-struct Runs {
-    int runs, rows;
-};
-Runs plan_runs(int T, int rows, int rpw) {
-    const int groups = (rows + rpw - 1) / rpw;  // warp-wide row groups of a token
-    const long long want = static_cast<long long>(num_sms()) * 32;
-    long long runs = T > 0 ? (want + T - 1) / T : 1;
-    if (runs > groups) runs = groups;
-    const int per = static_cast<int>((groups + runs - 1) / runs);
-    return {(groups + per - 1) / per, per * rpw};
+// Rows of a run: two batches of loads where there are many tokens, fewer (down to the rows
+// that a warp holds at once) until the warps fill the GPU.
+Runs plan_runs(const NormRope& p, int rpw, int batch, bool append) {
+    Runs r{};
+    for (r.rows = 2 * batch * rpw;; r.rows /= 2) {
+        const int kv = (p.a.Hkv + r.rows - 1) / r.rows;
+        r.q = (p.a.Hq + r.rows - 1) / r.rows;
+        r.k = p.k.p ? kv : 0;
+        r.v = append ? kv : 0;
+        if (r.rows <= rpw || static_cast<long long>(p.T) * r.total() >= num_sms() * 32ll) return r;
+    }
 }
 
 template <int LPR, int SWAP>
 cudaError_t fwd(const NormRope& p, bool append, cudaStream_t st) {
-    const int rows = p.a.Hq + (p.k.p ? p.a.Hkv : 0) + (append ? p.a.Hkv : 0);
-    const Runs r = plan_runs(p.T, rows, 32 / LPR);
-    const long long tasks = static_cast<long long>(p.T) * r.runs;
+    const Runs r = plan_runs(p, 32 / LPR, 4, append);
+    const long long tasks = static_cast<long long>(p.T) * r.total();
     const dim3 grid(static_cast<unsigned>((tasks + kWarps - 1) / kWarps));
     LaunchScope ls(append ? "kv_append" : "norm_rope", st);
-    return append ? launch_k(norm_rope_kernel<LPR, SWAP, true>, grid, dim3(kWarps * 32), 0, st, p,
-                             r.runs, r.rows)
-                  : launch_k(norm_rope_kernel<LPR, SWAP, false>, grid, dim3(kWarps * 32), 0, st, p,
-                             r.runs, r.rows);
+    return append ? launch_k(norm_rope_kernel<LPR, SWAP, true>, grid, dim3(kWarps * 32), 0, st, p, r,
+                             r.total())
+                  : launch_k(norm_rope_kernel<LPR, SWAP, false>, grid, dim3(kWarps * 32), 0, st, p, r,
+                             r.total());
 }
 
 template <int LPR, int SWAP>
 cudaError_t bwd(const NormRope& p, Heads dq_out, Heads dk_out, float* part, cudaStream_t st) {
-    const int rows = p.a.Hq + (p.k.p ? p.a.Hkv : 0);
-    const Runs r = plan_runs(p.T, rows, 32 / LPR);
+    const Runs r = plan_runs(p, 32 / LPR, 2, false);
     LaunchScope ls("norm_rope_backward", st);
     return launch_k(norm_rope_backward_kernel<LPR, SWAP>, dim3(norm_rope_parts(p.a, p.T)),
-                    dim3(kWarps * 32), 0, st, p, dq_out, dk_out, part, r.runs, r.rows);
+                    dim3(kWarps * 32), 0, st, p, dq_out, dk_out, part, r);
 }
 
 }  // namespace
@@ -400,13 +484,13 @@ cudaError_t launch_norm_rope(const NormRope& p, bool append, cudaStream_t st) {
     }
 }
 
-// CTAs of the backward (each writes one partial row): four per SM, fewer when there
+// CTAs of the backward (each writes one partial row): two per SM, fewer when there
 // are fewer rows.
 int norm_rope_parts(const moe_attn_shape& a, int T) {
     const int rpw = a.D <= 64 ? 4 : 2;
     const long long groups = static_cast<long long>(T) * ((a.Hq + a.Hkv + rpw - 1) / rpw);
     const long long ctas = (groups + kWarps - 1) / kWarps;
-    const long long most = 4ll * num_sms();
+    const long long most = 2ll * num_sms();
     return static_cast<int>(ctas < 1 ? 1 : ctas < most ? ctas : most);
 }
 
