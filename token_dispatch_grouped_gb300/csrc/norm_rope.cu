@@ -126,6 +126,13 @@ __device__ __forceinline__ void partners(const uint4& in, const float (&x)[8], i
     }
 }
 
+__device__ __forceinline__ void load_weights(const float* w, int piece, float (&v)[8]) {
+    const float4* s = reinterpret_cast<const float4*>(w + piece * 8);
+    const float4 x = __ldg(s), y = __ldg(s + 1);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+}
+
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
@@ -140,19 +147,18 @@ struct Runs {
     int total() const { return q + k + v; }
 };
 
-template <int LPR, int SWAP, bool APPEND>
-__global__ void __launch_bounds__(kWarps * 32, 3)
-norm_rope_kernel(const NormRope p, const Runs rn, int runs) {
+// U: row loads in flight per lane. A block takes one run of kWarps tokens.
+template <int LPR, int SWAP, bool APPEND, int U>
+__global__ void __launch_bounds__(kWarps * 32, U == 2 ? 4 : 3)
+norm_rope_kernel(const NormRope p, const Runs rn) {
     constexpr int RPW = 32 / LPR;  // rows of a warp at once
-    constexpr int U = 4;           // loads in flight per lane
     __shared__ __align__(16) bf16 s_buf[SWAP == SWAP_ROW ? kWarps * RPW * 128 : 8];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long task = static_cast<long long>(blockIdx.x) * kWarps + warp;
-    const int t = static_cast<int>(task / runs);
-    if (t >= p.T || has_error(p.err)) return;
-    int run = static_cast<int>(task % runs), kind = 0;  // 0 queries, 1 keys, 2 values
+    const int t = blockIdx.x * kWarps + warp;
+    if (t >= p.T) return;
+    int run = blockIdx.y, kind = 0;  // 0 queries, 1 keys, 2 values
     if (run >= rn.q) {
         run -= rn.q;
         kind = 1;
@@ -177,14 +183,32 @@ norm_rope_kernel(const NormRope p, const Runs rn, int runs) {
                 in[u] = *reinterpret_cast<const uint4*>(in_row + (rb - r0 + u * RPW) * src.hs);
         }
     };
+    // what does not depend on another load comes first, all of it in flight at once
     load(r0);
+    const bool skip = has_error(p.err);
+    const int pos = SWAP != SWAP_NONE && kind < 2 ? p.positions[t] : 0;
+    const long long slot = APPEND && kind > 0 ? p.slots[t] : 0;
+    const bool norm = p.wq != nullptr;
+    float w[8], wp[8];  // the weights of this lane's values and of their partners
+    if (norm && kind < 2) {
+        const float* wr = kind == 0 ? p.wq : p.wk;
+        load_weights(wr, live ? piece : 0, w);
+        if constexpr (SWAP == SWAP_LANE) {
+            const int hop = p.rot >> 4;
+            load_weights(wr, !live ? 0 : piece < hop ? piece + hop : piece < 2 * hop ? piece - hop : piece, wp);
+        } else if constexpr (SWAP == SWAP_ROW) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                wp[e] = __ldg(wr + (live ? partner_of(piece * 8 + e, p.rot, p.interleaved) : 0));
+        }
+    }
+    if (skip) return;
 
     // where the rows go
     bf16* out = (kind == 0 ? p.q_out : p.k_out).row(t, r0 + sub) + piece * 8;
     long long out_hs = (kind == 0 ? p.q_out : p.k_out).hs;
     if constexpr (APPEND) {
         if (kind > 0) {
-            const long long slot = p.slots[t];
             if (slot >= (static_cast<long long>(p.pages) << p.page_shift)) {
                 if (lane == 0) raise_error(p.err, MOE_ERR_BAD_INDEX);
                 return;
@@ -206,10 +230,8 @@ norm_rope_kernel(const NormRope p, const Runs rn, int runs) {
             return;
         }
     }
-    const bool norm = p.wq != nullptr;
     float a[8], b[8];  // A and B
     if constexpr (SWAP != SWAP_NONE) {
-        const int pos = p.positions[t];
         if (pos < 0 || pos >= p.table_rows) {  // the whole warp: one token
             if (lane == 0) raise_error(p.err, MOE_ERR_BAD_INDEX);
             return;
@@ -220,17 +242,12 @@ norm_rope_kernel(const NormRope p, const Runs rn, int runs) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) a[e] = 1.f;
     }
-    if (norm && live) {
-        const float* w = kind == 0 ? p.wq : p.wk;
+    if (norm) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            a[e] *= __ldg(w + piece * 8 + e);
-            if constexpr (SWAP != SWAP_NONE) {
-                int at = piece * 8 + e;
-                if constexpr (SWAP == SWAP_OWN) at = piece * 8 < p.rot ? at ^ 1 : at;
-                else at = partner_of(at, p.rot, p.interleaved);
-                b[e] *= __ldg(w + at);
-            }
+        for (int e = 0; e < 8; e += 2) {
+            mul2(a[e], a[e + 1], w[e], w[e + 1]);
+            if constexpr (SWAP == SWAP_OWN) mul2(b[e], b[e + 1], w[e + 1], w[e]);
+            if constexpr (SWAP == SWAP_LANE || SWAP == SWAP_ROW) mul2(b[e], b[e + 1], wp[e], wp[e + 1]);
         }
     }
     bf16* buf = s_buf + (SWAP == SWAP_ROW ? (warp * RPW + sub) * 128 : 0);
@@ -444,16 +461,23 @@ Runs plan_runs(const NormRope& p, int rpw, int batch, bool append) {
     }
 }
 
+template <int LPR, int SWAP, bool APPEND, int U>
+cudaError_t fwd_u(const NormRope& p, const Runs& r, cudaStream_t st) {
+    const dim3 grid(static_cast<unsigned>((p.T + kWarps - 1) / kWarps), r.total());
+    return launch_k(norm_rope_kernel<LPR, SWAP, APPEND, U>, grid, dim3(kWarps * 32), 0, st, p, r);
+}
+
+// Two loads in flight per lane where a token's heads are no more than that (fewer
+// registers, so more warps: XXX), else four.
 template <int LPR, int SWAP>
 cudaError_t fwd(const NormRope& p, bool append, cudaStream_t st) {
-    const Runs r = plan_runs(p, 32 / LPR, 4, append);
-    const long long tasks = static_cast<long long>(p.T) * r.total();
-    const dim3 grid(static_cast<unsigned>((tasks + kWarps - 1) / kWarps));
+    constexpr int RPW = 32 / LPR;
+    const Runs r = plan_runs(p, RPW, 4, append);
+    const bool few = p.a.Hq <= 2 * RPW || r.rows <= 2 * RPW;
     LaunchScope ls(append ? "kv_append" : "norm_rope", st);
-    return append ? launch_k(norm_rope_kernel<LPR, SWAP, true>, grid, dim3(kWarps * 32), 0, st, p, r,
-                             r.total())
-                  : launch_k(norm_rope_kernel<LPR, SWAP, false>, grid, dim3(kWarps * 32), 0, st, p, r,
-                             r.total());
+    if (append)
+        return few ? fwd_u<LPR, SWAP, true, 2>(p, r, st) : fwd_u<LPR, SWAP, true, 4>(p, r, st);
+    return few ? fwd_u<LPR, SWAP, false, 2>(p, r, st) : fwd_u<LPR, SWAP, false, 4>(p, r, st);
 }
 
 template <int LPR, int SWAP>
