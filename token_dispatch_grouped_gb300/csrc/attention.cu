@@ -103,7 +103,7 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
     if (warp == 0) {
         if ((sQ & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
         const bool skip = has_error(p.err);
-        Work w = find_work(p.s, false, 2 * tpt, blockIdx.x / p.a.Hkv, lane, p.err);
+        Work w = find_work<false>(p.s, 2 * tpt, blockIdx.x / p.a.Hkv, lane, p.err);
         if (skip) w.items = 0;
         if (lane == 0) *found = w;
     }
@@ -115,7 +115,7 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
     const Work w = *found;
     if (w.items > 0) {
         const int q0 = w.q0, nq = w.nq, k0 = w.k0, nk = w.nk;
-        const int base = (w.items - 1 - w.item) * 2 * tpt;  // the longest rows first
+        const int base = w.item * 2 * tpt;
         // keys that some row of a tile sees, and their tiles
         const auto limit_of = [&](int first) {
             const int last = min(first + tpt, nq) - 1;
@@ -347,7 +347,7 @@ cudaError_t forward(const Attention& p, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     LaunchScope ls("attention_forward", st);
-    return launch_k(kfn, dim3(static_cast<unsigned>(items * p.a.Hkv)), dim3(kThreads), C::SMEM, st,
+    return launch_pdl(kfn, dim3(static_cast<unsigned>(items * p.a.Hkv)), dim3(kThreads), C::SMEM, st,
                     mq, mk, mv, prm);
 }
 

@@ -132,7 +132,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
     if (warp == 0) {
         if ((sQ & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
         const bool skip = has_error(p.err);
-        Work w = find_work(p.s, false, tpt, blockIdx.x / p.a.Hkv, lane, p.err);
+        Work w = find_work<false>(p.s, tpt, blockIdx.x / p.a.Hkv, lane, p.err);
         if (skip) w.items = 0;
         if (lane == 0) *found = w;
     }
@@ -144,7 +144,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
     const Work w = *found;
     if (w.items > 0) {
         const int q0 = w.q0, nq = w.nq, k0 = w.k0, nk = w.nk;
-        const int first = (w.items - 1 - w.item) * tpt;  // the longest rows first
+        const int first = w.item * tpt;
         const int seen = p.s.causal ? max(0, min(nk, min(first + tpt, nq) + nk - nq)) : nk;
         const int n = (seen + kRows - 1) / kRows;
 
@@ -401,7 +401,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
     if (warp == 0) {
         if ((sK & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
         const bool skip = has_error(p.err);
-        Work w = find_work(p.s, true, kRows, blockIdx.x / p.a.Hkv, lane, p.err);
+        Work w = find_work<true>(p.s, tpt, blockIdx.x / p.a.Hkv, lane, p.err);
         if (skip) w.items = 0;
         if (lane == 0) *found = w;
     }
@@ -413,7 +413,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
     const Work w = *found;
     if (w.items > 0) {
         const int q0 = w.q0, nq = w.nq, k0 = w.k0, nk = w.nk;
-        const int kv0 = w.item * kRows;  // the first keys are seen most, and come first
+        const int kv0 = w.item * kRows;
         // query tiles [i0, i0 + n)
         const int i0 = (p.s.causal ? max(0, kv0 - (nk - nq)) : 0) / tpt;
         const int n = max(0, (nq + tpt - 1) / tpt - i0);
@@ -628,7 +628,7 @@ cudaError_t backward(const Attention& p, cudaStream_t st) {
                                              C::SMEM_Q);
         if (e != cudaSuccess) return e;
         LaunchScope ls("attention_dq", st);
-        e = launch_k(kfn, dim3(static_cast<unsigned>(qi * p.a.Hkv)), dim3(kThreads), C::SMEM_Q, st,
+        e = launch_pdl(kfn, dim3(static_cast<unsigned>(qi * p.a.Hkv)), dim3(kThreads), C::SMEM_Q, st,
                      mq, md, mk, mv, prm);
         if (e != cudaSuccess) return e;
     }
@@ -639,7 +639,7 @@ cudaError_t backward(const Attention& p, cudaStream_t st) {
                                                C::SMEM_KV);
     if (e != cudaSuccess) return e;
     LaunchScope ls("attention_dkv", st);
-    return launch_k(kfn, dim3(static_cast<unsigned>(ki * p.a.Hkv)), dim3(kThreads), C::SMEM_KV, st,
+    return launch_pdl(kfn, dim3(static_cast<unsigned>(ki * p.a.Hkv)), dim3(kThreads), C::SMEM_KV, st,
                     mq, md, mk, mv, prm);
 }
 

@@ -213,16 +213,60 @@ struct Work {
     int q0, nq, k0, nk;
     int item, items;  // items 0: nothing to do
 };
-// Work item `want` when a sequence has ceil(n / tile) items, n its query (or key) tokens:
-// one warp. Sequences that are not valid have none.
-__device__ __forceinline__ Work find_work(const Packed& s, bool keys, int tile, int want, int lane,
-                                          int* err) {
+
+// Items of one sequence whose steps are v >= 1 or more, out of `items`: tiles of `tile`
+// query tokens, whose steps are the 128-key tiles that they see (never fewer from one item
+// to the next, so these are the last ones) ...
+__device__ __forceinline__ int query_items(const Packed& s, const Work& w, int tile, int v) {
+    const int keys = (v - 1) * kRows + 1;  // sees at least as many
+    if (!s.causal) return w.nk >= keys ? w.items : 0;
+    const int need = keys - (w.nk - w.nq);  // tokens up to the end of the item
+    if (need > w.nq) return 0;
+    return need <= 0 ? w.items : w.items - ((need + tile - 1) / tile - 1);
+}
+// ... or tiles of 128 keys, whose steps are the query tiles that see them (never more from
+// one item to the next, so these are the first ones).
+__device__ __forceinline__ int key_items(const Packed& s, const Work& w, int tile, int v) {
+    const int tiles = (w.nq + tile - 1) / tile;
+    if (tiles < v) return 0;
+    if (!s.causal) return w.items;
+    const int keys = (tiles - v + 1) * tile + w.nk - w.nq;  // that start before it
+    return keys <= 0 ? 0 : min(w.items, (keys + kRows - 1) / kRows);
+}
+
+// Work item `want` of the batch, by one warp. Sequences that are not valid have none.
+// Up to 32 sequences (one a lane) the items with the most steps come first, over all of
+// them: the number of steps at rank `want` is found by bisection, then the sequence. (In
+// sequence order a long sequence at the batch's end starts last: XXX.) Beyond, the items
+// of a sequence follow each other, most steps first.
+template <bool KEYS>
+__device__ __forceinline__ Work find_work(const Packed& s, int tile, int want, int lane, int* err) {
+    const int size = KEYS ? kRows : tile;
     int before = 0;
     for (int b0 = 0; b0 < s.B; b0 += 32) {
-        int n = 0, q0 = 0, nq = 0, k0 = 0, nk = 0;
-        if (b0 + lane < s.B && sequence_of(s, b0 + lane, q0, nq, k0, nk, err))
-            n = ((keys ? nk : nq) + tile - 1) / tile;
-        int incl = n;
+        Work w{0, 0, 0, 0, 0, 0};
+        if (b0 + lane < s.B && sequence_of(s, b0 + lane, w.q0, w.nq, w.k0, w.nk, err))
+            w.items = ((KEYS ? w.nk : w.nq) + size - 1) / size;
+        const auto from_steps = [&](int v) {
+            return v < 1 ? w.items : w.items == 0 ? 0 : KEYS ? key_items(s, w, tile, v)
+                                                             : query_items(s, w, tile, v);
+        };
+        int mine = w.items, skipped = 0;  // items of this level (of all), and of higher ones
+        if (s.B <= 32 && s.B > 1) {
+            if (want >= __reduce_add_sync(0xffffffffu, w.items)) break;
+            // the largest v with more than `want` items of v steps or more
+            int lo = 0, hi = KEYS ? (w.nq + tile - 1) / tile : (w.nk + kRows - 1) / kRows;
+            hi = __reduce_max_sync(0xffffffffu, hi) + 1;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (__reduce_add_sync(0xffffffffu, from_steps(mid)) > want) lo = mid;
+                else hi = mid;
+            }
+            skipped = from_steps(lo + 1);
+            mine = from_steps(lo) - skipped;
+            before = __reduce_add_sync(0xffffffffu, skipped);
+        }
+        int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -231,13 +275,15 @@ __device__ __forceinline__ Work find_work(const Packed& s, bool keys, int tile, 
         const uint32_t past = __ballot_sync(0xffffffffu, want < before + incl);
         if (past) {
             const int l = __ffs(past) - 1;
-            Work w;
-            w.q0 = __shfl_sync(0xffffffffu, q0, l);
-            w.nq = __shfl_sync(0xffffffffu, nq, l);
-            w.k0 = __shfl_sync(0xffffffffu, k0, l);
-            w.nk = __shfl_sync(0xffffffffu, nk, l);
-            w.items = __shfl_sync(0xffffffffu, n, l);
-            w.item = want - (before + __shfl_sync(0xffffffffu, incl, l) - w.items);
+            // rank within the sequence, most steps first
+            w.item = want - (before + incl - mine) + skipped;
+            if (!KEYS) w.item = w.items - 1 - w.item;
+            w.q0 = __shfl_sync(0xffffffffu, w.q0, l);
+            w.nq = __shfl_sync(0xffffffffu, w.nq, l);
+            w.k0 = __shfl_sync(0xffffffffu, w.k0, l);
+            w.nk = __shfl_sync(0xffffffffu, w.nk, l);
+            w.item = __shfl_sync(0xffffffffu, w.item, l);
+            w.items = __shfl_sync(0xffffffffu, w.items, l);
             return w;
         }
         before += __shfl_sync(0xffffffffu, incl, 31);

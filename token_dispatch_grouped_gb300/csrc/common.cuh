@@ -42,9 +42,9 @@ inline bool pdl_enabled(bool gemm_launch = false) {
 // kernel<<<grid, block, smem, st>>>(args...), with programmatic stream
 // serialization where pdl_enabled() says so; the kernel calls pdl_wait() before
 // it touches global memory.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                     Args&&... args) {
+template <bool GEMM_LAUNCH, typename... KArgs, typename... Args>
+cudaError_t launch_as(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                      Args&&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
@@ -54,8 +54,19 @@ cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl_enabled() ? 1 : 0;
+    cfg.numAttrs = pdl_enabled(GEMM_LAUNCH) ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                     Args&&... args) {
+    return launch_as<false>(kernel, grid, block, smem, st, static_cast<KArgs>(args)...);
+}
+// The same for kernels that are launched programmatically by default, as the grouped GEMMs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                       Args&&... args) {
+    return launch_as<true>(kernel, grid, block, smem, st, static_cast<KArgs>(args)...);
 }
 
 // Device status word layout: the first error code that was raised wins.

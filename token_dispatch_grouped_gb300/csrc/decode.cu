@@ -369,13 +369,20 @@ __global__ void __launch_bounds__(128) join_kernel(const Params p) {
         const float f = exp2_fast(e.x - b2);
         const float w = e.y == 0.f ? 0.f : f * e.y;
         const int m = min(32, parts - i0);
-#pragma unroll 4
-        for (int i = 0; i < m; ++i) {
-            const float fi = __shfl_sync(~0u, f, i);
-            sum += __shfl_sync(~0u, w, i);
-            if (lane * 4 < D) {
-                const float4 x = *reinterpret_cast<const float4*>(src + static_cast<long long>(i0 + i) * D);
-                acc.x += fi * x.x, acc.y += fi * x.y, acc.z += fi * x.z, acc.w += fi * x.w;
+        for (int i1 = 0; i1 < m; i1 += 8) {  // eight parts' loads in flight
+            float4 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i1 + i < m && lane * 4 < D)
+                    x[i] = *reinterpret_cast<const float4*>(src + static_cast<long long>(i0 + i1 + i) * D);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float fi = __shfl_sync(~0u, f, i1 + i), wi = __shfl_sync(~0u, w, i1 + i);
+                if (i1 + i >= m) break;
+                sum += wi;
+                acc.x += fi * x[i].x, acc.y += fi * x[i].y, acc.z += fi * x[i].z, acc.w += fi * x[i].w;
             }
         }
     }
@@ -425,11 +432,11 @@ cudaError_t decode(const Decode& d, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     {
         LaunchScope ls("attention_decode", st);
-        e = launch_k(kfn, dim3(static_cast<unsigned>(items)), dim3(kThreads), C::SMEM, st, mk, mv, p);
+        e = launch_pdl(kfn, dim3(static_cast<unsigned>(items)), dim3(kThreads), C::SMEM, st, mk, mv, p);
         if (e != cudaSuccess || pl.parts == 1) return e;
     }
     LaunchScope ls("attention_join", st);
-    return launch_k(join_kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, st, p);
+    return launch_pdl(join_kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, st, p);
 }
 
 }  // namespace

@@ -530,7 +530,7 @@ cudaError_t launch_norm_rope_backward(const NormRope& p, Heads dq_out, Heads dk_
     }
     if (e != cudaSuccess || p.wq == nullptr) return e;
     LaunchScope ls("norm_rope_dw", st);
-    return launch_k(norm_rope_dw_kernel, dim3((2 * p.a.D + 31) / 32), dim3(1024), 0, st,
+    return launch_pdl(norm_rope_dw_kernel, dim3((2 * p.a.D + 31) / 32), dim3(1024), 0, st,
                     static_cast<const float*>(part), norm_rope_parts(p.a, p.T), p.a.D, dwq, dwk,
                     p.err);
 }
