@@ -6,11 +6,15 @@
 // c = scale log2(e), weights p = 2^(c S - c m), sum l += sum p, O += p v, and O and l
 // scaled by 2^(c m_old - c m_new) when m moves; out = O / l, lse = scale m + ln l.
 //
-// A CTA owns two tiles of 128 query rows of one key/value head. A tile's rows are the G
+// A CTA (one per SM) walks items of work, most steps first, dealt in snake order (dealt in
+// one direction the first CTA of 16384 tokens had 15% more steps than the mean); an item
+// is two tiles of 128 query rows of one key/value head. A tile's rows are the G
 // query heads of 128 / G tokens (token-major), so grouped heads share every key and value
 // tile that is loaded, and a short sequence still fills its tiles. Both tiles use each
 // 128-key tile of K and V from shared memory. Roles:
-//   warp 9     loads: Q once, then K and V tiles by TMA, two or three in flight of each;
+//   warp 9     finds the next item and loads its first tiles while the others finish the
+//              last one (a CTA per item spent 7.6 us outside its steps: 53 us for the packed
+//              batch of 4096 tokens against XXX); Q once, then K and V tiles by TMA;
 //   warp 8     the tensor cores: S_x = Q_x K^T (both from shared memory) into TMEM,
 //              O_x += P_x V with P_x as the TMEM operand;
 //   warps 0-3  softmax of tile 0, warps 4-7 of tile 1, one row a thread: S_x to registers,
@@ -29,13 +33,18 @@
 // l sums the unrounded p. Masks: a row's keys past its limit get S = -inf, by selection,
 // so what those rows hold does not matter; rows of V past the last key of the CTA are
 // zeroed in shared memory, since 0 * NaN would reach the sum.
+#include <algorithm>
+
 #include "attn_mma.cuh"
 
 namespace moe {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 320;
+// Three groups of four warps; the third (warps 10 and 11 idle) gives registers to the
+// softmax warps, which hold a row of 128 scores each: 256 * 200 + 128 * 104 = 384 * 168.
+constexpr int kThreads = 384;
+constexpr int kSoftRegs = 200, kOtherRegs = 104;
 
 template <int DP>  // D padded to 64 or 128
 struct Cfg {
@@ -43,7 +52,7 @@ struct Cfg {
     static constexpr int TILE = PIECES * kPiece;
     static constexpr int KR = 3, VR = 2;  // tiles of K and V in shared memory
     static constexpr int TILES = (2 + KR + VR) * TILE;
-    static constexpr int SMEM = TILES + 256;
+    static constexpr int SMEM = TILES + 512;
     static constexpr uint32_t TM_S = 0, TM_O = 256;
 };
 
@@ -54,7 +63,16 @@ struct Params {
     Heads out;
     float* lse;
     int* err;
-    int tpt;  // tokens of a 128-row tile
+    int tpt;    // tokens of a 128-row tile
+    int items;  // upper bound of the work items of a head
+};
+
+// One item: two query tiles of a key/value head, and the key tiles that they see.
+struct Item {
+    int q0, nq, k0, nk;
+    int base, hk;           // first token (in the sequence), key/value head (-1: no more work)
+    int tiles0, tiles1;     // key tiles that some row of each query tile sees
+    int steps, seen;        // the larger of them; keys that some row sees
 };
 
 template <int DP>
@@ -67,24 +85,30 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
     const uint32_t sQ = smem_u32(smem), sK = sQ + 2 * C::TILE, sV = sK + C::KR * C::TILE;
     uint8_t* misc = smem + C::TILES;
     const uint32_t bars = smem_u32(misc);
+    // Phases run on through all items of a CTA: steps are counted from its first item on
+    // (K and V tiles, step), tiles of scores per query tile (s, p), items per query tile
+    // that have any (q, q_free, o, o_free).
     const auto k_full = [&](int s) { return bars + 8u * s; };
     const auto v_full = [&](int s) { return bars + 8u * (3 + s); };
-    const auto step = [&](int s) { return bars + 8u * (5 + s); };         // step j's products done
-    const auto q_bar = [&](int x) { return bars + 8u * (7 + x); };
-    const auto s_bar = [&](int x) { return bars + 8u * (9 + x); };        // S_x written
-    const auto o_bar = [&](int x) { return bars + 8u * (11 + x); };       // O_x final
-    const auto p_bar = [&](int x, int h) { return bars + 8u * (13 + 2 * x + h); };  // half of P_x
+    const auto step = [&](int s) { return bars + 8u * (5 + s); };      // a step's products done
+    const auto q_full = [&](int x) { return bars + 8u * (7 + x); };
+    const auto q_free = [&](int x) { return bars + 8u * (9 + x); };    // Q_x read for the last time
+    const auto s_bar = [&](int x) { return bars + 8u * (11 + x); };    // S_x written
+    const auto o_bar = [&](int x) { return bars + 8u * (13 + x); };    // O_x final
+    const auto w_full = [&](int s) { return bars + 8u * (15 + s); };   // an item is in its slot
     const uint32_t done_bar = bars + 8u * 17, tail_bar = bars + 8u * 18;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 8 * 19);
+    const auto p_bar = [&](int x, int h) { return bars + 8u * (19 + 2 * x + h); };  // half of P_x
+    const auto o_free = [&](int x) { return bars + 8u * (23 + x); };   // O_x read
+    const auto w_free = [&](int s) { return bars + 8u * (25 + s); };   // its slot read
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 8 * 27);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    Work* found = reinterpret_cast<Work*>(tmem_slot + 2);
+    Item* ring = reinterpret_cast<Item*>(misc + 8 * 28);  // two slots
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 13; ++i) mbar_init(bars + 8 * i, 1);
-        for (int i = 13; i < 17; ++i) mbar_init(bars + 8 * i, 4);  // the tile's warps
-        mbar_init(done_bar, 1);
-        mbar_init(tail_bar, 1);
+        for (int i = 0; i < 19; ++i) mbar_init(bars + 8 * i, 1);
+        for (int i = 19; i < 25; ++i) mbar_init(bars + 8 * i, 4);  // the tile's warps
+        for (int i = 25; i < 27; ++i) mbar_init(bars + 8 * i, 9);  // all warps but the loads'
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -97,156 +121,206 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
         prefetch_tensormap(&mapK);
         prefetch_tensormap(&mapV);
     }
-    pdl_wait();
-    pdl_trigger();
-    const int hk = blockIdx.x % p.a.Hkv, tpt = p.tpt, G = p.a.Hq / p.a.Hkv;
-    if (warp == 0) {
-        if ((sQ & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
-        const bool skip = has_error(p.err);
-        Work w = find_work<false>(p.s, 2 * tpt, blockIdx.x / p.a.Hkv, lane, p.err);
-        if (skip) w.items = 0;
-        if (lane == 0) *found = w;
-    }
-    if (warp == 1 && blockIdx.x == 0) check_sequences(p.s, lane, p.err);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_wait();
+    pdl_trigger();
     const uint32_t tmem = *tmem_slot;
-    const Work w = *found;
-    if (w.items > 0) {
-        const int q0 = w.q0, nq = w.nq, k0 = w.k0, nk = w.nk;
-        const int base = w.item * 2 * tpt;
-        // keys that some row of a tile sees, and their tiles
-        const auto limit_of = [&](int first) {
-            const int last = min(first + tpt, nq) - 1;
-            return last < first ? 0 : p.s.causal ? max(0, min(nk, last + 1 + nk - nq)) : nk;
-        };
-        const int limit0 = limit_of(base), limit1 = limit_of(base + tpt);
-        const int tiles0 = (limit0 + kRows - 1) / kRows, tiles1 = (limit1 + kRows - 1) / kRows;
-        const int n = max(tiles0, tiles1), seen = max(limit0, limit1);
-        const bool ragged = seen % kRows != 0;  // the last V tile has rows past the keys
+    const int tpt = p.tpt, G = p.a.Hq / p.a.Hkv;
+    // Item i of this CTA, for those that only read them (false: no more work), and its
+    // slot given back by a warp.
+    const auto item_there = [&](int i) -> bool {
+        wait_phase(w_full(i & 1), (i >> 1) & 1, abort_flag);
+        return ring[i & 1].hk >= 0 && *abort_flag == 0;
+    };
+    const auto item_done = [&](int i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(w_free(i & 1));
+    };
 
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 9) {
-            // ------------------------------------------------------------ loads
-            if (lane == 0) {
-                const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int h, int t) {
-                    for (int c = 0; c < C::PIECES; ++c)
-                        tma_load_3d(dst + c * kPiece, m, bar, 64 * c, h, t);
-                };
-                const uint32_t qbytes = C::PIECES * 128 * G * tpt;
-                int jk = 0, jv = 0;
-                const auto load_q = [&](int x) {
-                    mbar_arrive_expect_tx(q_bar(x), qbytes);
-                    load(sQ + x * C::TILE, &mapQ, q_bar(x), hk * G, q0 + base + x * tpt);
-                };
-                const auto load_k = [&](int j) {
-                    mbar_arrive_expect_tx(k_full(j % C::KR), C::TILE);
-                    load(sK + j % C::KR * C::TILE, &mapK, k_full(j % C::KR), hk, k0 + j * kRows);
-                    ++jk;
-                };
-                if (tiles0 > 0) load_q(0);
-                if (n > 0) load_k(0);
-                if (tiles1 > 0) load_q(1);
-                for (int j = 0; j < n; ++j) {
-                    // step j - 2 is the last that reads V_{j-2}; K_{j-2} was read before it
-                    if (j >= 2) wait_phase(step(j & 1), (j / 2 - 1) & 1, abort_flag);
-                    if (*abort_flag) break;
-                    mbar_arrive_expect_tx(v_full(j & 1), C::TILE);
-                    load(sV + (j & 1) * C::TILE, &mapV, v_full(j & 1), hk, k0 + j * kRows);
-                    ++jv;
-                    if (j + 1 < n) load_k(j + 1);
+            // ---------------------------------------------------------------- loads
+            if ((sQ & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
+            const bool skip = __any_sync(~0u, has_error(p.err));
+            if (blockIdx.x == 0) check_sequences(p.s, lane, p.err);
+            const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int h, int t) {
+                for (int c = 0; c < C::PIECES; ++c)
+                    tma_load_3d(dst + c * kPiece, m, bar, 64 * c, h, t);
+            };
+            const uint32_t qbytes = C::PIECES * 128 * G * tpt;
+            int g = 0, kg = 0, qg0 = 0, qg1 = 0;  // steps, K tiles, Q tiles loaded so far
+            for (int i = 0;; ++i) {
+                // find the item (keys seen per query tile) while the others work on the last one
+                // snake order: forwards through the CTAs, then backwards
+                const int index = i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                Item it{};
+                it.hk = -1;
+                if (!skip && index < p.items * p.a.Hkv) {
+                    const Work w = find_work<false>(p.s, 2 * tpt, index / p.a.Hkv, lane, p.err);
+                    it.q0 = w.q0, it.nq = w.nq, it.k0 = w.k0, it.nk = w.nk;
+                    it.base = w.item * 2 * tpt;
+                    if (w.items > 0) it.hk = index % p.a.Hkv;
+                    const auto limit_of = [&](int first) {
+                        const int last = min(first + tpt, it.nq) - 1;
+                        return last < first ? 0
+                               : p.s.causal ? max(0, min(it.nk, last + 1 + it.nk - it.nq))
+                                            : it.nk;
+                    };
+                    const int limit0 = limit_of(it.base), limit1 = limit_of(it.base + tpt);
+                    it.tiles0 = (limit0 + kRows - 1) / kRows;
+                    it.tiles1 = (limit1 + kRows - 1) / kRows;
+                    it.steps = max(it.tiles0, it.tiles1);
+                    it.seen = max(limit0, limit1);
                 }
-                // nothing is in flight when the CTA leaves
-                if (tiles0 > 0) drain(q_bar(0), 0);
-                if (tiles1 > 0) drain(q_bar(1), 0);
-                for (int j = max(0, jk - C::KR); j < jk; ++j) drain(k_full(j % C::KR), (j / C::KR) & 1);
-                for (int j = max(0, jv - C::VR); j < jv; ++j) drain(v_full(j & 1), (j >> 1) & 1);
-            }
-            __syncwarp();
-            if (ragged) {
-                // the last V tile has landed (or the CTA has given up)
-                zero_tail(sV + ((n - 1) & 1) * C::TILE, C::PIECES, seen % kRows, lane);
-                if (lane == 0) mbar_arrive(tail_bar);
-            }
-        } else if (warp == 8) {
-            // ----------------------------------------------------- tensor cores
-            constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, DP, 0, 1);
-            const auto scores = [&](int x, int j) {
-                const uint64_t ad = desc_d(sQ + x * C::TILE), bd = desc_d(sK + j % C::KR * C::TILE);
-                const uint32_t dst = tmem + C::TM_S + 128 * x, bar = s_bar(x);
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < DP / 16; ++k) mma_bf16(dst, ad + kd(k), bd + kd(k), id_s, k > 0);
-                    mma_commit(bar);
+                if (i >= 2) warp_wait(w_free(i & 1), (i / 2 - 1) & 1, abort_flag);
+                if (lane == 0) {
+                    ring[i & 1] = it;
+                    mbar_arrive(w_full(i & 1));
                 }
                 __syncwarp();
-            };
-            if (n > 0) warp_wait(k_full(0), 0, abort_flag);
-            if (tiles0 > 0) {
-                warp_wait(q_bar(0), 0, abort_flag);
-                tc_fence_after();
-                scores(0, 0);
+                if (it.hk < 0 || *abort_flag) break;
+                if (lane == 0) {
+                    const auto load_q = [&](int x, int& count) {
+                        if (count > 0) wait_phase(q_free(x), (count - 1) & 1, abort_flag);
+                        if (*abort_flag) return;
+                        ++count;
+                        mbar_arrive_expect_tx(q_full(x), qbytes);
+                        load(sQ + x * C::TILE, &mapQ, q_full(x), it.hk * G, it.q0 + it.base + x * tpt);
+                    };
+                    const auto load_k = [&](int j) {
+                        mbar_arrive_expect_tx(k_full(kg % C::KR), C::TILE);
+                        load(sK + kg % C::KR * C::TILE, &mapK, k_full(kg % C::KR), it.hk,
+                             it.k0 + j * kRows);
+                        ++kg;
+                    };
+                    // K tile g is loaded when step g - 3 is done: it was waited for at step g - 1
+                    if (it.steps > 0 && *abort_flag == 0) load_k(0);
+                    if (it.tiles0 > 0) load_q(0, qg0);
+                    if (it.tiles1 > 0) load_q(1, qg1);
+                    for (int j = 0; j < it.steps; ++j) {
+                        // step g - 2 is the last that reads V tile g - 2; K tile g - 2 was read
+                        // before it
+                        if (g >= 2) wait_phase(step(g & 1), (g / 2 - 1) & 1, abort_flag);
+                        if (*abort_flag) break;
+                        mbar_arrive_expect_tx(v_full(g & 1), C::TILE);
+                        load(sV + (g & 1) * C::TILE, &mapV, v_full(g & 1), it.hk, it.k0 + j * kRows);
+                        ++g;
+                        if (j + 1 < it.steps) load_k(j + 1);
+                    }
+                }
+                __syncwarp();
+                if (it.seen % kRows != 0) {  // the last V tile has rows past the keys
+                    const int last = __shfl_sync(~0u, g, 0) - 1;
+                    if (last >= 0) {
+                        warp_wait(v_full(last & 1), (last >> 1) & 1, abort_flag);
+                        zero_tail(sV + (last & 1) * C::TILE, C::PIECES, it.seen % kRows, lane);
+                    }
+                    if (lane == 0) mbar_arrive(tail_bar);
+                }
             }
-            if (tiles1 > 0) {
-                warp_wait(q_bar(1), 0, abort_flag);
-                tc_fence_after();
-                scores(1, 0);
+            if (lane == 0) {  // nothing is in flight when the CTA leaves
+                if (qg0 > 0) drain(q_full(0), (qg0 - 1) & 1);
+                if (qg1 > 0) drain(q_full(1), (qg1 - 1) & 1);
+                for (int j = max(0, kg - C::KR); j < kg; ++j) drain(k_full(j % C::KR), (j / C::KR) & 1);
+                for (int j = max(0, g - C::VR); j < g; ++j) drain(v_full(j & 1), (j >> 1) & 1);
             }
-            for (int j = 0; j < n; ++j) {
-                warp_wait(v_full(j & 1), (j >> 1) & 1, abort_flag);
-                if (j + 1 < n) warp_wait(k_full((j + 1) % C::KR), ((j + 1) / C::KR) & 1, abort_flag);
-                else if (ragged) warp_wait(tail_bar, 0, abort_flag);
-                const uint64_t vd = desc_r(sV + (j & 1) * C::TILE);
-                const uint32_t add = j > 0;
+            __syncwarp();
+        } else if (warp == 8 && elect_one()) {
+            // ----------------------------------------------- tensor cores (one thread)
+            constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, DP, 0, 1);
+            int g = 0, tails = 0, had0 = 0, had1 = 0, ps0 = 0, ps1 = 0;  // see the phases above
+            const auto scores = [&](int x, int kt, bool last) {
+                const uint64_t ad = desc_d(sQ + x * C::TILE), bd = desc_d(sK + kt % C::KR * C::TILE);
+                const uint32_t dst = tmem + C::TM_S + 128 * x;
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int tiles = x == 0 ? tiles0 : tiles1;
-                    if (j >= tiles) continue;
-                    const uint32_t dst = tmem + C::TM_O + DP * x, src = tmem + C::TM_S + 128 * x;
-                    const uint32_t bar = o_bar(x);
-                    const bool last = j + 1 == tiles;
-                    warp_wait(p_bar(x, 0), j & 1, abort_flag);
+                for (int k = 0; k < DP / 16; ++k) mma_bf16(dst, ad + kd(k), bd + kd(k), id_s, k > 0);
+                mma_commit(s_bar(x));
+                if (last) mma_commit(q_free(x));
+            };
+            for (int i = 0; item_there(i); ++i) {
+                const Item& it = ring[i & 1];
+                const int n = it.steps, tiles0 = it.tiles0, tiles1 = it.tiles1;
+                const bool ragged = it.seen % kRows != 0;
+                mbar_arrive(w_free(i & 1));
+                if (n > 0) wait_phase(k_full(g % C::KR), (g / C::KR) & 1, abort_flag);
+                if (tiles0 > 0) {
+                    wait_phase(q_full(0), had0 & 1, abort_flag);
                     tc_fence_after();
-                    if (elect_one()) {
+                    scores(0, g, tiles0 == 1);
+                }
+                if (tiles1 > 0) {
+                    wait_phase(q_full(1), had1 & 1, abort_flag);
+                    tc_fence_after();
+                    scores(1, g, tiles1 == 1);
+                }
+                for (int j = 0; j < n; ++j, ++g) {
+                    wait_phase(v_full(g & 1), (g >> 1) & 1, abort_flag);
+                    if (j + 1 < n) {
+                        wait_phase(k_full((g + 1) % C::KR), ((g + 1) / C::KR) & 1, abort_flag);
+                    } else if (ragged) {
+                        wait_phase(tail_bar, tails & 1, abort_flag);
+                        ++tails;
+                    }
+                    const uint64_t vd = desc_r(sV + (g & 1) * C::TILE);
+                    const uint32_t add = j > 0;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int tiles = x == 0 ? tiles0 : tiles1;
+                        if (j >= tiles) continue;
+                        const int ps = x == 0 ? ps0 : ps1;
+                        const int had = x == 0 ? had0 : had1;
+                        const uint32_t dst = tmem + C::TM_O + DP * x, src = tmem + C::TM_S + 128 * x;
+                        const bool last = j + 1 == tiles;
+                        // the last item's O_x has been read
+                        if (j == 0 && had > 0) wait_phase(o_free(x), (had - 1) & 1, abort_flag);
+                        wait_phase(p_bar(x, 0), ps & 1, abort_flag);
+                        tc_fence_after();
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             mma_bf16_ta(dst, src + 8 * k, vd + kr(k), id_o, k > 0 ? 1u : add);
-                    }
-                    __syncwarp();
-                    warp_wait(p_bar(x, 1), j & 1, abort_flag);
-                    tc_fence_after();
-                    if (elect_one()) {
+                        wait_phase(p_bar(x, 1), ps & 1, abort_flag);
+                        tc_fence_after();
 #pragma unroll
-                        for (int k = 4; k < 8; ++k) mma_bf16_ta(dst, src + 8 * k, vd + kr(k), id_o, 1u);
-                        if (last) mma_commit(bar);
+                        for (int k = 4; k < 8; ++k)
+                            mma_bf16_ta(dst, src + 8 * k, vd + kr(k), id_o, 1u);
+                        if (x == 0) ++ps0;
+                        else ++ps1;
+                        if (last) mma_commit(o_bar(x));
+                        else scores(x, g + 1, j + 2 == tiles);
                     }
-                    __syncwarp();
-                    if (!last) scores(x, j + 1);
+                    mma_commit(step(g & 1));
                 }
-                const uint32_t bar = step(j & 1);
-                if (elect_one()) mma_commit(bar);
-                __syncwarp();
+                had0 += tiles0 > 0;
+                had1 += tiles1 > 0;
             }
-            if (elect_one()) mma_commit(done_bar);
-            __syncwarp();
+            mma_commit(done_bar);
             drain(done_bar, 0);
-            __syncwarp();
-        } else {
-            // ---------------------------------------------------------- softmax
-            const int x = warp >> 2;
-            const int row = threadIdx.x & 127, head = row % G;
-            const int first = base + x * tpt, token = first + row / G;  // in the sequence
-            const int tiles = x == 0 ? tiles0 : tiles1;
-            const bool valid = row < G * tpt && token < nq;
-            const int mine = !valid ? 0 : p.s.causal ? min(nk, token + 1 + nk - nq) : nk;
-            // every row of the tile sees the keys before this one
-            const int open = p.s.causal ? first + 1 + nk - nq : nk;
-            const float c = p.scale * 1.44269504088896341f;
-            const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-            const uint32_t tS = lanes + C::TM_S + 128 * x, tO = lanes + C::TM_O + DP * x;
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        // -------------------------------------------------------------- softmax
+        const int x = warp >> 2;
+        const int row = threadIdx.x & 127, head = row % G, rtok = row / G;
+        const float c = p.scale * 1.44269504088896341f;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t tS = lanes + C::TM_S + 128 * x, tO = lanes + C::TM_O + DP * x;
+        int ps = 0, had = 0;
+        for (int i = 0; __all_sync(~0u, item_there(i)); ++i) {
+            const Item& it = ring[i & 1];
+            const int tiles = x == 0 ? it.tiles0 : it.tiles1;
+            int mine, open;  // keys that this row sees, and that every row of the tile sees
+            {
+                const int first = it.base + x * tpt, more = it.nk - it.nq;
+                const bool valid = row < G * tpt && first + rtok < it.nq;
+                mine = !valid ? 0 : p.s.causal ? min(it.nk, first + rtok + 1 + more) : it.nk;
+                open = p.s.causal ? first + 1 + more : it.nk;
+            }
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < tiles; ++j) {
-                warp_wait(s_bar(x), j & 1, abort_flag);
+            for (int j = 0; j < tiles; ++j, ++ps) {
+                warp_wait(s_bar(x), ps & 1, abort_flag);
                 tc_fence_after();
                 float s[128];
 #pragma unroll
@@ -256,13 +330,13 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
                 if ((j + 1) * kRows > open) {
                     const int lim = mine - j * kRows;
 #pragma unroll
-                    for (int i = 0; i < 128; ++i) s[i] = i < lim ? s[i] : -INFINITY;
+                    for (int e = 0; e < 128; ++e) s[e] = e < lim ? s[e] : -INFINITY;
                 }
                 float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                for (int i = 4; i < 124; i += 8)
+                for (int e = 4; e < 124; e += 8)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[i + 2 * u], s[i + 2 * u + 1]);
+                    for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[e + 2 * u], s[e + 2 * u + 1]);
                 const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], s[124], s[125]),
                                        fmaxf(s[126], s[127]));
                 if (j == 0) {
@@ -278,8 +352,8 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
                         tmem_ld16(tO + q, o);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                        for (int e = 0; e < 16; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
                         tmem_st16(tO + q, o);
                     }
                 }
@@ -290,11 +364,11 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
                     for (int q = 64 * h; q < 64 * h + 64; q += 32) {
                         uint32_t o[16];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            fma2v(s[q + i], s[q + i + 1], c, shift, shift);
-                            s[q + i] = exp2_fast(s[q + i]);
-                            s[q + i + 1] = exp2_fast(s[q + i + 1]);
-                            o[i / 2] = pack2(s[q + i], s[q + i + 1]);
+                        for (int e = 0; e < 32; e += 2) {
+                            fma2v(s[q + e], s[q + e + 1], c, shift, shift);
+                            s[q + e] = exp2_fast(s[q + e]);
+                            s[q + e + 1] = exp2_fast(s[q + e + 1]);
+                            o[e / 2] = pack2(s[q + e], s[q + e + 1]);
                         }
                         tmem_st16(tS + q / 2, o);
                     }
@@ -303,23 +377,43 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
                 }
                 float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
-                for (int i = 0; i < 128; i += 4) {
-                    add2(s0, s1, s[i], s[i + 1]);
-                    add2(s2, s3, s[i + 2], s[i + 3]);
+                for (int e = 0; e < 128; e += 4) {
+                    add2(s0, s1, s[e], s[e + 1]);
+                    add2(s2, s3, s[e + 2], s[e + 3]);
                 }
                 l += (s0 + s1) + (s2 + s3);
             }
-            if (tiles > 0) warp_wait(o_bar(x), 0, abort_flag);
-            if (first < nq) {
+            const int token = it.base + x * tpt + rtok, h = it.hk * G + head;
+            const bool valid = row < G * tpt && token < it.nq;
+            const long long t = it.q0 + token;
+            item_done(i);
+            if (valid)
+                p.lse[t * p.a.Hq + h] = l == 0.f ? -INFINITY : fmaf(m, p.scale, logf(l));
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            bf16* dst = p.out.row(t, h);
+            if (tiles > 0) {
+                warp_wait(o_bar(x), had & 1, abort_flag);
+                ++had;
                 tc_fence_after();
-                const long long t = q0 + token;
-                const int h = hk * G + head;
-                if (valid)
-                    p.lse[t * p.a.Hq + h] = l == 0.f ? -INFINITY : fmaf(m, p.scale, logf(l));
-                // The rows leave through Q_x, all reads of which are done.
-                store_rows<DP>(tO, tiles > 0, l == 0.f ? 0.f : 1.f / l,
-                               smem + x * C::TILE + (warp & 3) * 32 * DP * 2, lane,
-                               valid ? p.out.row(t, h) : nullptr, 0, p.a.D);
+            }
+#pragma unroll 1
+            for (int q = 0; q < DP; q += 32) {
+                uint32_t o[32];
+                if (tiles > 0) {
+                    tmem_ld32(tO + q, o);
+                    tmem_ld_wait();
+                    if (q + 32 == DP) warp_arrive(o_free(x), lane);
+                }
+                if (valid) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        float v[8];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u)
+                            v[u] = tiles > 0 && l != 0.f ? __uint_as_float(o[e + u]) * inv : 0.f;
+                        if (q + e < p.a.D) *reinterpret_cast<uint4*>(dst + q + e) = pack8(v);
+                    }
+                }
             }
         }
     }
@@ -333,22 +427,23 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
 template <int DP>
 cudaError_t forward(const Attention& p, cudaStream_t st) {
     using C = Cfg<DP>;
-    const int G = p.a.Hq / p.a.Hkv, D = p.a.D;
-    Params prm{p.a, p.s, p.scale, p.out, p.lse, p.err, kRows / G};
+    const int G = p.a.Hq / p.a.Hkv, D = p.a.D, tpt = kRows / G;
+    const long long items = tile_bound(p.s.Tq, p.s.B, p.s.max_q, 2 * tpt);
+    if (items == 0) return cudaSuccess;
+    Params prm{p.a, p.s, p.scale, p.out, p.lse, p.err, tpt, static_cast<int>(items)};
     CUtensorMap mq, mk, mv;
-    if (!make_tmap_heads(&mq, p.q, p.s.Tq, p.a.Hq, D, G, prm.tpt)) return cudaErrorInvalidValue;
+    if (!make_tmap_heads(&mq, p.q, p.s.Tq, p.a.Hq, D, G, tpt)) return cudaErrorInvalidValue;
     mk = mv = mq;  // without keys no tile is loaded
     if (p.s.Tk > 0 && (!make_tmap_heads(&mk, p.k, p.s.Tk, p.a.Hkv, D, 1, kRows) ||
                        !make_tmap_heads(&mv, p.v, p.s.Tk, p.a.Hkv, D, 1, kRows)))
         return cudaErrorInvalidValue;
-    const long long items = tile_bound(p.s.Tq, p.s.B, p.s.max_q, 2 * prm.tpt);
-    if (items == 0) return cudaSuccess;
     auto kfn = attention_forward_kernel<DP>;
     cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
+    const long long ctas = std::min<long long>(items * p.a.Hkv, num_sms());
     LaunchScope ls("attention_forward", st);
-    return launch_pdl(kfn, dim3(static_cast<unsigned>(items * p.a.Hkv)), dim3(kThreads), C::SMEM, st,
-                    mq, mk, mv, prm);
+    return launch_pdl(kfn, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), C::SMEM, st, mq, mk, mv,
+                      prm);
 }
 
 }  // namespace

@@ -189,41 +189,36 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                 zero_tail(sK + (n - 1) % C::R0 * C::TILE, C::PIECES, seen % kRows, lane);
                 if (lane == 0) mbar_arrive(tail_bar);
             }
-        } else if (warp == kCompute) {
+        } else if (warp == kCompute && elect_one()) {
             constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_q = idesc_bf16(128, DP, 0, 1);
+            const uint64_t qd = desc_d(sQ), dod = desc_d(sDO);
             // S_j and dP_j, once their keys and values are there (rows of K past the keys
             // zeroed: dQ sums over them)
             const auto scores = [&](int j) {
                 const int s = j % C::R0;
-                warp_wait(k_full(s), (j / C::R0) & 1, abort_flag);
-                if (j + 1 == n && seen % kRows != 0) warp_wait(tail_bar, 0, abort_flag);
+                wait_phase(k_full(s), (j / C::R0) & 1, abort_flag);
+                if (j + 1 == n && seen % kRows != 0) wait_phase(tail_bar, 0, abort_flag);
                 tc_fence_after();
-                const uint64_t ad = desc_d(sQ), bd = desc_d(sK + s * C::TILE);
-                if (elect_one()) {
+                const uint64_t bd = desc_d(sK + s * C::TILE);
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k)
-                        mma_bf16(tmem + TM_S, ad + kd(k), bd + kd(k), id_s, k > 0);
-                    mma_commit(s_bar);
-                }
-                __syncwarp();
+                for (int k = 0; k < DP / 16; ++k)
+                    mma_bf16(tmem + TM_S, qd + kd(k), bd + kd(k), id_s, k > 0);
+                mma_commit(s_bar);
             };
             const auto dprob = [&](int j) {
                 const int s = j % C::R1;
-                warp_wait(v_full(s), (j / C::R1) & 1, abort_flag);
+                wait_phase(v_full(s), (j / C::R1) & 1, abort_flag);
                 tc_fence_after();
-                const uint64_t ad = desc_d(sDO), bd = desc_d(sV + s * C::TILE);
-                const uint32_t dst = tmem + TM_DP + 128 * (j & 1), bar = dp_bar(j & 1);
-                if (elect_one()) {
+                const uint64_t bd = desc_d(sV + s * C::TILE);
+                const uint32_t dst = tmem + TM_DP + 128 * (j & 1);
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k) mma_bf16(dst, ad + kd(k), bd + kd(k), id_s, k > 0);
-                    mma_commit(bar);
-                }
-                __syncwarp();
+                for (int k = 0; k < DP / 16; ++k) mma_bf16(dst, dod + kd(k), bd + kd(k), id_s, k > 0);
+                mma_commit(dp_bar(j & 1));
             };
             if (n > 0) {
-                warp_wait(q_bar, 0, abort_flag);
+                wait_phase(q_bar, 0, abort_flag);
                 scores(0);
-                warp_wait(do_bar, 0, abort_flag);
+                wait_phase(do_bar, 0, abort_flag);
                 dprob(0);
             }
             for (int j = 0; j < n; ++j) {
@@ -231,27 +226,21 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
                 // the next tile's products run while dS_j is formed: S may be overwritten
                 // once it is in registers, and dP has two places
                 if (j + 1 < n) {
-                    warp_wait(s_read, j & 1, abort_flag);
+                    wait_phase(s_read, j & 1, abort_flag);
                     scores(j + 1);
                     dprob(j + 1);
                 }
-                warp_wait(ds_bar, j & 1, abort_flag);
+                wait_phase(ds_bar, j & 1, abort_flag);
                 tc_fence_after();
                 const uint64_t kdesc = desc_r(sK + sk * C::TILE);
-                const uint32_t ke = k_empty(sk), add = j > 0, src = tmem + TM_DP + 128 * (j & 1);
-                if (elect_one()) {
+                const uint32_t add = j > 0, src = tmem + TM_DP + 128 * (j & 1);
 #pragma unroll
-                    for (int k = 0; k < kRows / 16; ++k)
-                        mma_bf16_ta(tmem + TM_DQ, operand(src, k), kdesc + kr(k), id_q,
-                                    k > 0 ? 1u : add);
-                    mma_commit(ke);
-                }
-                __syncwarp();
+                for (int k = 0; k < kRows / 16; ++k)
+                    mma_bf16_ta(tmem + TM_DQ, operand(src, k), kdesc + kr(k), id_q, k > 0 ? 1u : add);
+                mma_commit(k_empty(sk));
             }
-            if (elect_one()) mma_commit(done_bar);
-            __syncwarp();
+            mma_commit(done_bar);
             drain(done_bar, 0);
-            __syncwarp();
         } else if (warp < kCompute) {
             const int grp = warp >> 2, row = threadIdx.x & 127;
             const int token = first + row / G, g = row % G;
@@ -475,67 +464,54 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
                 }
                 mbar_arrive(r_full(i & 1));
             }
-        } else if (warp == kCompute) {
+        } else if (warp == kCompute && elect_one()) {
             constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_g = idesc_bf16(128, DP, 0, 1);
+            const uint64_t kdesc = desc_d(sK), vd = desc_d(sV);
             // S^T_i, once its queries are there (rows past them zeroed: dK sums over them)
             const auto scores = [&](int i) {
                 const int s = i % C::R0;
-                warp_wait(q_full(s), (i / C::R0) & 1, abort_flag);
-                if (i + 1 == n && ragged) warp_wait(tail_bar, 0, abort_flag);
+                wait_phase(q_full(s), (i / C::R0) & 1, abort_flag);
+                if (i + 1 == n && ragged) wait_phase(tail_bar, 0, abort_flag);
                 tc_fence_after();
-                const uint64_t ad = desc_d(sK), bd = desc_d(sQ + s * C::TILE);
-                if (elect_one()) {
+                const uint64_t bd = desc_d(sQ + s * C::TILE);
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k)
-                        mma_bf16(tmem + TM_S, ad + kd(k), bd + kd(k), id_s, k > 0);
-                    mma_commit(s_bar);
-                }
-                __syncwarp();
+                for (int k = 0; k < DP / 16; ++k)
+                    mma_bf16(tmem + TM_S, kdesc + kd(k), bd + kd(k), id_s, k > 0);
+                mma_commit(s_bar);
             };
             if (n > 0) {
-                warp_wait(kv_bar, 0, abort_flag);
+                wait_phase(kv_bar, 0, abort_flag);
                 scores(0);
             }
             for (int i = 0; i < n; ++i) {
                 const int sd = i % C::R1, sq = i % C::R0;
-                const uint64_t vd = desc_d(sV), dod = desc_d(sDO + sd * C::TILE);
-                const uint64_t dor = desc_r(sDO + sd * C::TILE), qr = desc_r(sQ + sq * C::TILE);
-                const uint32_t de = do_empty(sd), qe = q_empty(sq), add = i > 0;
-                warp_wait(do_full(sd), (i / C::R1) & 1, abort_flag);
+                const uint64_t dod = desc_d(sDO + sd * C::TILE), dor = desc_r(sDO + sd * C::TILE);
+                const uint64_t qr = desc_r(sQ + sq * C::TILE);
+                const uint32_t add = i > 0;
+                wait_phase(do_full(sd), (i / C::R1) & 1, abort_flag);
                 tc_fence_after();
-                if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k)
-                        mma_bf16(tmem + TM_DP, vd + kd(k), dod + kd(k), id_s, k > 0);
-                    mma_commit(dp_bar);
-                }
-                __syncwarp();
-                warp_wait(p_bar, i & 1, abort_flag);
+                for (int k = 0; k < DP / 16; ++k)
+                    mma_bf16(tmem + TM_DP, vd + kd(k), dod + kd(k), id_s, k > 0);
+                mma_commit(dp_bar);
+                wait_phase(p_bar, i & 1, abort_flag);
                 tc_fence_after();
-                if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kRows / 16; ++k)
-                        mma_bf16_ta(tmem + TM_DV, operand(tmem + TM_S, k), dor + kr(k), id_g,
-                                    k > 0 ? 1u : add);
-                    mma_commit(de);
-                }
-                __syncwarp();
+                for (int k = 0; k < kRows / 16; ++k)
+                    mma_bf16_ta(tmem + TM_DV, operand(tmem + TM_S, k), dor + kr(k), id_g,
+                                k > 0 ? 1u : add);
+                mma_commit(do_empty(sd));
                 if (i + 1 < n) scores(i + 1);
-                warp_wait(ds_bar, i & 1, abort_flag);
+                wait_phase(ds_bar, i & 1, abort_flag);
                 tc_fence_after();
-                if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kRows / 16; ++k)
-                        mma_bf16_ta(tmem + TM_DK, operand(tmem + TM_DP, k), qr + kr(k), id_g,
-                                    k > 0 ? 1u : add);
-                    mma_commit(qe);
-                }
-                __syncwarp();
+                for (int k = 0; k < kRows / 16; ++k)
+                    mma_bf16_ta(tmem + TM_DK, operand(tmem + TM_DP, k), qr + kr(k), id_g,
+                                k > 0 ? 1u : add);
+                mma_commit(q_empty(sq));
             }
-            if (elect_one()) mma_commit(done_bar);
-            __syncwarp();
+            mma_commit(done_bar);
             drain(done_bar, 0);
-            __syncwarp();
         } else if (warp < kCompute) {
             const int grp = warp >> 2, row = threadIdx.x & 127;
             const int key = kv0 + row;  // in its sequence

@@ -29,10 +29,13 @@ __device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, ui
 }
 
 // One lane of a converged warp (the same one every time), in the form that lets the
-// tensor-core instructions take their operands from uniform registers: with 16 busy warps
-// beside the issuing one, a 128 x 128 x 16 product took 333 cycles to issue under
-// `lane == 0` with a descriptor built per step, 121 under elect.sync, and 81 with a step
-// as a constant added to a descriptor (64 is the tensor cores' own time).
+// tensor-core instructions take their operands from uniform registers. The role that
+// issues the products runs as a whole in such a thread: with 16 busy warps beside it and
+// a barrier polled every 8 products, a 128 x 128 x 16 product takes 66 cycles (64 is the
+// tensor cores' own time), against 143 with warp-wide waits and an election for every
+// group, and 333 under `lane == 0` with a descriptor built for every step. (The queue of
+// issued products is short, so what the thread does between them is lost to the tensor
+// cores.)
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
