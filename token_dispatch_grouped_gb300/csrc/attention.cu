@@ -12,9 +12,10 @@
 // query heads of 128 / G tokens (token-major), so grouped heads share every key and value
 // tile that is loaded, and a short sequence still fills its tiles. Both tiles use each
 // 128-key tile of K and V from shared memory. Roles:
-//   warp 9     finds the next item and loads its first tiles while the others finish the
-//              last one (a CTA per item spent 7.6 us outside its steps: 53 us for the packed
-//              batch of 4096 tokens against XXX); Q once, then K and V tiles by TMA;
+//   warp 10    finds the next item while the others work on the last one (a CTA per item
+//              spent 7.6 us outside its steps: 53 us for the packed batch of 4096 tokens
+//              against XXX);
+//   warp 9     loads: Q, then K and V tiles by TMA, into the next item as tiles fall free;
 //   warp 8     the tensor cores: S_x = Q_x K^T (both from shared memory) into TMEM,
 //              O_x += P_x V with P_x as the TMEM operand;
 //   warps 0-3  softmax of tile 0, warps 4-7 of tile 1, one row a thread: S_x to registers,
@@ -41,7 +42,7 @@ namespace moe {
 namespace attn {
 namespace {
 
-// Three groups of four warps; the third (warps 10 and 11 idle) gives registers to the
+// Three groups of four warps; the third (warp 11 idle) gives registers to the
 // softmax warps, which hold a row of 128 scores each: 256 * 200 + 128 * 104 = 384 * 168.
 constexpr int kThreads = 384;
 constexpr int kSoftRegs = 200, kOtherRegs = 104;
@@ -108,7 +109,7 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
     if (threadIdx.x == 0) {
         for (int i = 0; i < 19; ++i) mbar_init(bars + 8 * i, 1);
         for (int i = 19; i < 25; ++i) mbar_init(bars + 8 * i, 4);  // the tile's warps
-        for (int i = 25; i < 27; ++i) mbar_init(bars + 8 * i, 9);  // all warps but the loads'
+        for (int i = 25; i < 27; ++i) mbar_init(bars + 8 * i, 10);  // warps 0 to 9
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -141,29 +142,21 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == 9) {
-            // ---------------------------------------------------------------- loads
+        if (warp == 10) {
+            // ----------------------------------------- items, one ahead of the others
             if ((sQ & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
-            const bool skip = __any_sync(~0u, has_error(p.err));
-            if (blockIdx.x == 0) check_sequences(p.s, lane, p.err);
-            const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int h, int t) {
-                for (int c = 0; c < C::PIECES; ++c)
-                    tma_load_3d(dst + c * kPiece, m, bar, 64 * c, h, t);
-            };
-            const uint32_t qbytes = C::PIECES * 128 * G * tpt;
-            int g = 0, kg = 0, qg0 = 0, qg1 = 0;  // steps, K tiles, Q tiles loaded so far
+            const int skip = has_error(p.err);
             for (int i = 0;; ++i) {
-                // find the item (keys seen per query tile) while the others work on the last one
                 // snake order: forwards through the CTAs, then backwards
                 const int index = i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
                 Item it{};
                 it.hk = -1;
-                if (!skip && index < p.items * p.a.Hkv) {
+                if (index < p.items * p.a.Hkv) {
                     const Work w = find_work<false>(p.s, 2 * tpt, index / p.a.Hkv, lane, p.err);
                     it.q0 = w.q0, it.nq = w.nq, it.k0 = w.k0, it.nk = w.nk;
                     it.base = w.item * 2 * tpt;
-                    if (w.items > 0) it.hk = index % p.a.Hkv;
-                    const auto limit_of = [&](int first) {
+                    if (w.items > 0 && !skip) it.hk = index % p.a.Hkv;
+                    const auto limit_of = [&](int first) {  // keys that some row of a tile sees
                         const int last = min(first + tpt, it.nq) - 1;
                         return last < first ? 0
                                : p.s.causal ? max(0, min(it.nk, last + 1 + it.nk - it.nq))
@@ -180,8 +173,20 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
                     ring[i & 1] = it;
                     mbar_arrive(w_full(i & 1));
                 }
-                __syncwarp();
-                if (it.hk < 0 || *abort_flag) break;
+                if (__any_sync(~0u, it.hk < 0 || *abort_flag != 0)) break;
+            }
+            if (blockIdx.x == 0) check_sequences(p.s, lane, p.err);
+        } else if (warp == 9) {
+            // ---------------------------------------------------------------- loads
+            const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int h, int t) {
+                for (int c = 0; c < C::PIECES; ++c)
+                    tma_load_3d(dst + c * kPiece, m, bar, 64 * c, h, t);
+            };
+            const uint32_t qbytes = C::PIECES * 128 * G * tpt;
+            int g = 0, kg = 0, qg0 = 0, qg1 = 0;  // steps, K tiles, Q tiles loaded so far
+            for (int i = 0; __all_sync(~0u, item_there(i)); ++i) {
+                const Item it = ring[i & 1];
+                item_done(i);
                 if (lane == 0) {
                     const auto load_q = [&](int x, int& count) {
                         if (count > 0) wait_phase(q_free(x), (count - 1) & 1, abort_flag);
