@@ -97,17 +97,20 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
     const auto s_bar = [&](int x) { return bars + 8u * (11 + x); };    // S_x written
     const auto o_bar = [&](int x) { return bars + 8u * (13 + x); };    // O_x final
     const auto w_full = [&](int s) { return bars + 8u * (15 + s); };   // an item is in its slot
-    const uint32_t done_bar = bars + 8u * 17, tail_bar = bars + 8u * 18;
+    const uint32_t done_bar = bars + 8u * 17;
     const auto p_bar = [&](int x, int h) { return bars + 8u * (19 + 2 * x + h); };  // half of P_x
     const auto o_free = [&](int x) { return bars + 8u * (23 + x); };   // O_x read
     const auto w_free = [&](int s) { return bars + 8u * (25 + s); };   // its slot read
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 8 * 27);
+    const auto tail_bar = [&](int s) { return bars + 8u * (27 + s); };  // V's slot zeroed
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 8 * 29);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    Item* ring = reinterpret_cast<Item*>(misc + 8 * 28);  // two slots
+    Item* ring = reinterpret_cast<Item*>(misc + 8 * 30);  // two slots
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 19; ++i) mbar_init(bars + 8 * i, 1);
+        for (int i = 0; i < 18; ++i) mbar_init(bars + 8 * i, 1);
+        mbar_init(tail_bar(0), 1);
+        mbar_init(tail_bar(1), 1);
         for (int i = 19; i < 25; ++i) mbar_init(bars + 8 * i, 4);  // the tile's warps
         for (int i = 25; i < 27; ++i) mbar_init(bars + 8 * i, 10);  // warps 0 to 9
         *abort_flag = 0;
@@ -223,7 +226,7 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
                         warp_wait(v_full(last & 1), (last >> 1) & 1, abort_flag);
                         zero_tail(sV + (last & 1) * C::TILE, C::PIECES, it.seen % kRows, lane);
                     }
-                    if (lane == 0) mbar_arrive(tail_bar);
+                    if (lane == 0) mbar_arrive(tail_bar(last & 1));
                 }
             }
             if (lane == 0) {  // nothing is in flight when the CTA leaves
@@ -236,7 +239,8 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
         } else if (warp == 8 && elect_one()) {
             // ----------------------------------------------- tensor cores (one thread)
             constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, DP, 0, 1);
-            int g = 0, tails = 0, had0 = 0, had1 = 0, ps0 = 0, ps1 = 0;  // see the phases above
+            int g = 0, had0 = 0, had1 = 0, ps0 = 0, ps1 = 0;  // see the phases above
+            uint32_t tails = 0;  // the phase of each slot's next tail
             const auto scores = [&](int x, int kt, bool last) {
                 const uint64_t ad = desc_d(sQ + x * C::TILE), bd = desc_d(sK + kt % C::KR * C::TILE);
                 const uint32_t dst = tmem + C::TM_S + 128 * x;
@@ -266,8 +270,10 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
                     if (j + 1 < n) {
                         wait_phase(k_full((g + 1) % C::KR), ((g + 1) / C::KR) & 1, abort_flag);
                     } else if (ragged) {
-                        wait_phase(tail_bar, tails & 1, abort_flag);
-                        ++tails;
+                        // (a V slot is not loaded again before its step is done, so no
+                        // phase of its tail is passed)
+                        wait_phase(tail_bar(g & 1), tails >> (g & 1) & 1, abort_flag);
+                        tails ^= 1 << (g & 1);
                     }
                     const uint64_t vd = desc_r(sV + (g & 1) * C::TILE);
                     const uint32_t add = j > 0;

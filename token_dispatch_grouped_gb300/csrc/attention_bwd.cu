@@ -25,6 +25,8 @@
 // P and dS are rounded to bf16 (the operand type), everything else is fp32; scale enters
 // dq and dk once at the end. Masked weights are zero by selection, and rows of an operand
 // that lie past the sequence are zeroed in shared memory where they are summed over.
+#include <algorithm>
+
 #include "attn_mma.cuh"
 
 namespace moe {
@@ -45,7 +47,8 @@ struct Params {
     const float* lse;
     float *row_lse, *row_delta;  // [Hkv][Tq][G]: -lse * log2(e) (-inf: no key) and -delta
     int* err;
-    int tpt;  // tokens of a 128-row query tile
+    int tpt;    // tokens of a 128-row query tile
+    int items;  // upper bound of a head's query tiles (dq_kernel)
 };
 
 template <int DP>
@@ -54,7 +57,7 @@ struct Cfg {
     static constexpr int TILE = PIECES * kPiece;
     static constexpr int R0 = 3, R1 = 2;  // ring stages: the operand used twice, the other
     static constexpr int TILES = (2 + R0 + R1) * TILE;
-    static constexpr int SMEM_Q = TILES + 4 * 512 + 256;       // parts of delta, barriers
+    static constexpr int SMEM_Q = TILES + kGroups * 512 + 512;  // parts of delta, barriers
     static constexpr int SMEM_KV = TILES + 2 * 2 * 512 + 256;  // two slots of lse and delta
 };
 
@@ -83,6 +86,13 @@ __device__ __forceinline__ uint32_t operand(uint32_t t, int k) {
 }
 
 // ---------------------------------------------------------------------- dq
+// One tile of 128 query rows and the key tiles that it sees.
+struct Item {
+    int q0, nq, k0, nk;
+    int first, hk;    // first token (in the sequence), key/value head (-1: no more work)
+    int steps, seen;  // key tiles and keys that some row sees
+};
+
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapDO,
@@ -92,33 +102,34 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sQ = smem_u32(smem), sDO = sQ + C::TILE;
     const uint32_t sK = sDO + C::TILE, sV = sK + C::R0 * C::TILE;
-    float* part_delta = reinterpret_cast<float*>(smem + C::TILES);  // [4][128]
-    uint8_t* misc = smem + C::TILES + 4 * 512;
+    float* part_delta = reinterpret_cast<float*>(smem + C::TILES);  // [kGroups][128]
+    uint8_t* misc = smem + C::TILES + kGroups * 512;
     const uint32_t bars = smem_u32(misc);
+    // Phases run on through all items of a CTA: steps are counted from its first item on,
+    // q, do, q_free, dq, dq_free and tail per item that has steps (tail: that needs it).
     const auto k_full = [&](int s) { return bars + 8u * s; };
     const auto k_empty = [&](int s) { return bars + 8u * (3 + s); };
     const auto v_full = [&](int s) { return bars + 8u * (6 + s); };
-    const auto dp_bar = [&](int s) { return bars + 8u * (10 + s); };
-    const uint32_t q_bar = bars + 96, do_bar = bars + 104, s_bar = bars + 112,
-                   ds_bar = bars + 120, done_bar = bars + 128, s_read = bars + 136,
-                   tail_bar = bars + 144;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 152);
+    const auto dp_bar = [&](int s) { return bars + 8u * (8 + s); };    // dP written (V read)
+    const auto w_full = [&](int s) { return bars + 8u * (10 + s); };   // an item is in its slot
+    const uint32_t q_bar = bars + 8u * 12, do_bar = bars + 8u * 13, q_free = bars + 8u * 14,
+                   s_bar = bars + 8u * 15, dq_bar = bars + 8u * 16, tail_bar = bars + 8u * 17,
+                   done_bar = bars + 8u * 18;
+    const uint32_t s_read = bars + 8u * 19, delta_bar = bars + 8u * 20, dq_free = bars + 8u * 21;
+    // dS written: two, as the dS of two steps can be finished before the products' thread
+    // looks again (a wait that is passed by two phases would not return)
+    const auto ds_bar = [&](int s) { return bars + 8u * (22 + s); };
+    const auto w_free = [&](int s) { return bars + 8u * (24 + s); };   // an item's slot read
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 8 * 26);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    Work* found = reinterpret_cast<Work*>(tmem_slot + 2);
+    Item* ring = reinterpret_cast<Item*>(misc + 8 * 27);  // two slots
     constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DQ = 384;  // dP twice
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 8; ++i) mbar_init(bars + 8 * i, 1);
-        mbar_init(dp_bar(0), 1);
-        mbar_init(dp_bar(1), 1);
-        mbar_init(q_bar, 1);
-        mbar_init(do_bar, 1);
-        mbar_init(s_bar, 1);
-        mbar_init(ds_bar, kCompute);
-        mbar_init(done_bar, 1);
-        mbar_init(s_read, kCompute);
-        mbar_init(tail_bar, 1);
+        for (int i = 0; i < 19; ++i) mbar_init(bars + 8 * i, 1);
+        for (int i = 19; i < 24; ++i) mbar_init(bars + 8 * i, kCompute);
+        for (int i = 24; i < 26; ++i) mbar_init(bars + 8 * i, kCompute + 2);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -126,204 +137,278 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
-    pdl_wait();
-    pdl_trigger();
-    const int hk = blockIdx.x % p.a.Hkv, tpt = p.tpt, G = p.a.Hq / p.a.Hkv;
-    if (warp == 0) {
-        if ((sQ & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
-        const bool skip = has_error(p.err);
-        Work w = find_work<false>(p.s, tpt, blockIdx.x / p.a.Hkv, lane, p.err);
-        if (skip) w.items = 0;
-        if (lane == 0) *found = w;
+    if (warp == kCompute + 1 && lane == 0) {
+        prefetch_tensormap(&mapQ);
+        prefetch_tensormap(&mapDO);
+        prefetch_tensormap(&mapK);
+        prefetch_tensormap(&mapV);
     }
-    if (warp == 1 && blockIdx.x == 0) check_sequences(p.s, lane, p.err);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_wait();
+    pdl_trigger();
     const uint32_t tmem = *tmem_slot;
-    const Work w = *found;
-    if (w.items > 0) {
-        const int q0 = w.q0, nq = w.nq, k0 = w.k0, nk = w.nk;
-        const int first = w.item * tpt;
-        const int seen = p.s.causal ? max(0, min(nk, min(first + tpt, nq) + nk - nq)) : nk;
-        const int n = (seen + kRows - 1) / kRows;
+    const int tpt = p.tpt, G = p.a.Hq / p.a.Hkv;
+    const auto item_there = [&](int i) -> bool {
+        wait_phase(w_full(i & 1), (i >> 1) & 1, abort_flag);
+        return ring[i & 1].hk >= 0 && *abort_flag == 0;
+    };
+    const auto item_done = [&](int i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(w_free(i & 1));
+    };
 
-        if (warp == kCompute + 1) {
-            const bool ragged = seen % kRows != 0;  // the last K tile has rows past the keys
-            if (lane == 0 && n > 0) {
-                const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int h, int t) {
-                    for (int c = 0; c < C::PIECES; ++c)
-                        tma_load_3d(dst + c * kPiece, m, bar, 64 * c, h, t);
-                };
-                const uint32_t qbytes = C::PIECES * 128 * G * tpt;
-                mbar_arrive_expect_tx(q_bar, qbytes);
-                load(sQ, &mapQ, q_bar, hk * G, q0 + first);
-                int jk = 0, jv = 0;
-                for (int j = 0; j < n; ++j) {
-                    int s = j % C::R0;
-                    if (j >= C::R0) wait_phase(k_empty(s), (j / C::R0 - 1) & 1, abort_flag);
+    if (warp == kCompute + 2) {
+        // --------------------------------------------- items, one ahead of the others
+        if ((sQ & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
+        const int skip = has_error(p.err);
+        for (int i = 0;; ++i) {
+            // snake order: forwards through the CTAs, then backwards
+            const int index = i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            Item it{};
+            it.hk = -1;
+            if (index < p.items * p.a.Hkv) {
+                const Work w = find_work<false>(p.s, tpt, index / p.a.Hkv, lane, p.err);
+                it.q0 = w.q0, it.nq = w.nq, it.k0 = w.k0, it.nk = w.nk;
+                it.first = w.item * tpt;
+                if (w.items > 0 && !skip) it.hk = index % p.a.Hkv;
+                it.seen = p.s.causal ? max(0, min(w.nk, min(it.first + tpt, w.nq) + w.nk - w.nq)) : w.nk;
+                it.steps = (it.seen + kRows - 1) / kRows;
+            }
+            if (i >= 2) warp_wait(w_free(i & 1), (i / 2 - 1) & 1, abort_flag);
+            if (lane == 0) {
+                ring[i & 1] = it;
+                mbar_arrive(w_full(i & 1));
+            }
+            if (__any_sync(~0u, it.hk < 0 || *abort_flag != 0)) break;
+        }
+        if (blockIdx.x == 0) check_sequences(p.s, lane, p.err);
+    } else if (warp == kCompute + 1) {
+        // ---------------------------------------------------------------------- loads
+        const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int h, int t) {
+            for (int c = 0; c < C::PIECES; ++c) tma_load_3d(dst + c * kPiece, m, bar, 64 * c, h, t);
+        };
+        const uint32_t qbytes = C::PIECES * 128 * G * tpt;
+        int gk = 0, gv = 0, had = 0, dos = 0;  // K and V tiles, Q and dO tiles loaded so far
+        for (int i = 0; __all_sync(~0u, item_there(i)); ++i) {
+            const Item it = ring[i & 1];
+            item_done(i);
+            if (lane == 0 && it.steps > 0) {
+                for (int j = 0; j < it.steps; ++j) {
+                    int s = gk % C::R0;
+                    if (gk >= C::R0) wait_phase(k_empty(s), (gk / C::R0 - 1) & 1, abort_flag);
                     if (*abort_flag) break;
                     mbar_arrive_expect_tx(k_full(s), C::TILE);
-                    load(sK + s * C::TILE, &mapK, k_full(s), hk, k0 + j * kRows);
-                    ++jk;
+                    load(sK + s * C::TILE, &mapK, k_full(s), it.hk, it.k0 + j * kRows);
+                    ++gk;
                     if (j == 0) {
+                        if (had > 0) wait_phase(q_free, (had - 1) & 1, abort_flag);
+                        if (*abort_flag) break;
+                        ++had;
+                        mbar_arrive_expect_tx(q_bar, qbytes);
+                        load(sQ, &mapQ, q_bar, it.hk * G, it.q0 + it.first);
+                        ++dos;
                         mbar_arrive_expect_tx(do_bar, qbytes);
-                        load(sDO, &mapDO, do_bar, hk * G, q0 + first);
+                        load(sDO, &mapDO, do_bar, it.hk * G, it.q0 + it.first);
                     }
-                    s = j % C::R1;  // V_{j-2} has been read when dP_{j-2} is there
-                    if (j >= C::R1) wait_phase(dp_bar(s), (j / C::R1 - 1) & 1, abort_flag);
+                    s = gv % C::R1;  // V tile g - 2 has been read when its dP is there
+                    if (gv >= C::R1) wait_phase(dp_bar(s), (gv / C::R1 - 1) & 1, abort_flag);
                     if (*abort_flag) break;
                     mbar_arrive_expect_tx(v_full(s), C::TILE);
-                    load(sV + s * C::TILE, &mapV, v_full(s), hk, k0 + j * kRows);
-                    ++jv;
+                    load(sV + s * C::TILE, &mapV, v_full(s), it.hk, it.k0 + j * kRows);
+                    ++gv;
                 }
-                // nothing is in flight when the CTA leaves
-                drain(q_bar, 0);
-                if (jk > 0) drain(do_bar, 0);
-                for (int j = max(0, jk - C::R0); j < jk; ++j) drain(k_full(j % C::R0), (j / C::R0) & 1);
-                for (int j = max(0, jv - C::R1); j < jv; ++j) drain(v_full(j % C::R1), (j / C::R1) & 1);
             }
             __syncwarp();
-            if (ragged) {
-                // the last K tile has landed (or the CTA has given up)
-                zero_tail(sK + (n - 1) % C::R0 * C::TILE, C::PIECES, seen % kRows, lane);
+            if (it.seen % kRows != 0) {  // the last K tile has rows past the keys
+                const int last = __shfl_sync(~0u, gk, 0) - 1;
+                if (last >= 0) {
+                    warp_wait(k_full(last % C::R0), (last / C::R0) & 1, abort_flag);
+                    zero_tail(sK + last % C::R0 * C::TILE, C::PIECES, it.seen % kRows, lane);
+                }
                 if (lane == 0) mbar_arrive(tail_bar);
             }
-        } else if (warp == kCompute && elect_one()) {
-            constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_q = idesc_bf16(128, DP, 0, 1);
-            const uint64_t qd = desc_d(sQ), dod = desc_d(sDO);
-            // S_j and dP_j, once their keys and values are there (rows of K past the keys
-            // zeroed: dQ sums over them)
-            const auto scores = [&](int j) {
-                const int s = j % C::R0;
-                wait_phase(k_full(s), (j / C::R0) & 1, abort_flag);
-                if (j + 1 == n && seen % kRows != 0) wait_phase(tail_bar, 0, abort_flag);
+        }
+        if (lane == 0) {  // nothing is in flight when the CTA leaves
+            if (had > 0) drain(q_bar, (had - 1) & 1);
+            if (dos > 0) drain(do_bar, (dos - 1) & 1);
+            for (int j = max(0, gk - C::R0); j < gk; ++j) drain(k_full(j % C::R0), (j / C::R0) & 1);
+            for (int j = max(0, gv - C::R1); j < gv; ++j) drain(v_full(j % C::R1), (j / C::R1) & 1);
+        }
+        __syncwarp();
+    } else if (warp == kCompute && elect_one()) {
+        // ------------------------------------------------- tensor cores (one thread)
+        constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_q = idesc_bf16(128, DP, 0, 1);
+        const uint64_t qd = desc_d(sQ), dod = desc_d(sDO);
+        int g = 0, had = 0, tails = 0;
+        for (int i = 0; item_there(i); ++i) {
+            const int n = ring[i & 1].steps;
+            const bool ragged = ring[i & 1].seen % kRows != 0;
+            mbar_arrive(w_free(i & 1));
+            // S and dP of step t (the item's last: `last`), once their keys and values are
+            // there (rows of K past the keys zeroed: dQ sums over them); S may be
+            // overwritten once it is in registers, and dP has two places
+            const auto scores = [&](int t, bool last) {
+                if (t > 0) wait_phase(s_read, (t - 1) & 1, abort_flag);
+                wait_phase(k_full(t % C::R0), (t / C::R0) & 1, abort_flag);
+                if (last && ragged) wait_phase(tail_bar, tails & 1, abort_flag);
                 tc_fence_after();
-                const uint64_t bd = desc_d(sK + s * C::TILE);
+                const uint64_t bd = desc_d(sK + t % C::R0 * C::TILE);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
                     mma_bf16(tmem + TM_S, qd + kd(k), bd + kd(k), id_s, k > 0);
                 mma_commit(s_bar);
             };
-            const auto dprob = [&](int j) {
-                const int s = j % C::R1;
-                wait_phase(v_full(s), (j / C::R1) & 1, abort_flag);
+            const auto dprob = [&](int t, bool last) {
+                wait_phase(v_full(t & 1), (t >> 1) & 1, abort_flag);
                 tc_fence_after();
-                const uint64_t bd = desc_d(sV + s * C::TILE);
-                const uint32_t dst = tmem + TM_DP + 128 * (j & 1);
+                const uint64_t bd = desc_d(sV + (t & 1) * C::TILE);
+                const uint32_t dst = tmem + TM_DP + 128 * (t & 1);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) mma_bf16(dst, dod + kd(k), bd + kd(k), id_s, k > 0);
-                mma_commit(dp_bar(j & 1));
+                mma_commit(dp_bar(t & 1));
+                if (last) mma_commit(q_free);
             };
-            if (n > 0) {
-                wait_phase(q_bar, 0, abort_flag);
-                scores(0);
-                wait_phase(do_bar, 0, abort_flag);
-                dprob(0);
-            }
-            for (int j = 0; j < n; ++j) {
-                const int sk = j % C::R0;
-                // the next tile's products run while dS_j is formed: S may be overwritten
-                // once it is in registers, and dP has two places
+            if (n == 0) continue;
+            wait_phase(q_bar, had & 1, abort_flag);
+            scores(g, n == 1);
+            wait_phase(do_bar, had & 1, abort_flag);
+            dprob(g, n == 1);
+            for (int j = 0; j < n; ++j, ++g) {
+                // the next tile's products run while dS is formed
                 if (j + 1 < n) {
-                    wait_phase(s_read, j & 1, abort_flag);
-                    scores(j + 1);
-                    dprob(j + 1);
+                    scores(g + 1, j + 2 == n);
+                    dprob(g + 1, j + 2 == n);
                 }
-                wait_phase(ds_bar, j & 1, abort_flag);
+                // the last item's dQ has been read
+                if (j == 0 && had > 0) wait_phase(dq_free, (had - 1) & 1, abort_flag);
+                wait_phase(ds_bar(g & 1), (g >> 1) & 1, abort_flag);
                 tc_fence_after();
-                const uint64_t kdesc = desc_r(sK + sk * C::TILE);
-                const uint32_t add = j > 0, src = tmem + TM_DP + 128 * (j & 1);
+                const uint64_t kdesc = desc_r(sK + g % C::R0 * C::TILE);
+                const uint32_t add = j > 0, src = tmem + TM_DP + 128 * (g & 1);
 #pragma unroll
                 for (int k = 0; k < kRows / 16; ++k)
                     mma_bf16_ta(tmem + TM_DQ, operand(src, k), kdesc + kr(k), id_q, k > 0 ? 1u : add);
-                mma_commit(k_empty(sk));
+                mma_commit(k_empty(g % C::R0));
             }
-            mma_commit(done_bar);
-            drain(done_bar, 0);
-        } else if (warp < kCompute) {
-            const int grp = warp >> 2, row = threadIdx.x & 127;
-            const int token = first + row / G, g = row % G;
-            const bool valid = row < G * tpt && token < nq;
-            const int mine = !valid ? 0 : p.s.causal ? min(nk, token + 1 + nk - nq) : nk;
-            const int open = p.s.causal ? first + 1 + nk - nq : nk;  // keys that every row sees
-            const float c = p.scale * kLog2e;
-            const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-            // delta: each group sums its part of the row's columns, all loads at once
+            mma_commit(dq_bar);
+            ++had;
+            tails += ragged;
+        }
+        mma_commit(done_bar);
+        drain(done_bar, 0);
+    } else if (warp < kCompute) {
+        // -------------------------------------------------------------- weights to dS
+        const int grp = warp >> 2, row = threadIdx.x & 127, rtok = row / G, head = row % G;
+        const float c = p.scale * kLog2e;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        constexpr int W = DP / kGroups;  // columns of dq that a group stores
+        int g = 0, had = 0;
+        for (int i = 0; __all_sync(~0u, item_there(i)); ++i) {
+            const Item it = ring[i & 1];
+            item_done(i);
+            const int n = it.steps, token = it.first + rtok;
+            const bool valid = row < G * tpt && token < it.nq;
+            const int mine = !valid ? 0 : p.s.causal ? min(it.nk, token + 1 + it.nk - it.nq) : it.nk;
+            const int open = p.s.causal ? it.first + 1 + it.nk - it.nq : it.nk;  // seen by every row
+            const long long t = it.q0 + token;
+            const int h = it.hk * G + head;
+            // delta: each group sums its part of the row's columns, all loads at once. (The
+            // sums of the last item have been read: its dQ is complete. Rows of an item
+            // without steps see no key, and their out is 0.)
             float delta = 0.f, neg_lse = -INFINITY;
-            {
-                constexpr int V = DP / kGroups / 8;
+            if (n > 0) {
+                constexpr int V = W / 8;
                 uint4 o[V], d[V];
-                const bf16* po = p.out.row(q0 + token, hk * G + g);
-                const bf16* pd = p.dout.row(q0 + token, hk * G + g);
+                const bf16* po = p.out.row(t, h);
+                const bf16* pd = p.dout.row(t, h);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int col = (grp * V + i) * 8;
-                    o[i] = d[i] = make_uint4(0u, 0u, 0u, 0u);
+                for (int u = 0; u < V; ++u) {
+                    const int col = (grp * V + u) * 8;
+                    o[u] = d[u] = make_uint4(0u, 0u, 0u, 0u);
                     if (valid && col < p.a.D) {
-                        o[i] = *reinterpret_cast<const uint4*>(po + col);
-                        d[i] = *reinterpret_cast<const uint4*>(pd + col);
+                        o[u] = *reinterpret_cast<const uint4*>(po + col);
+                        d[u] = *reinterpret_cast<const uint4*>(pd + col);
                     }
                 }
                 if (valid) {
-                    const float e = p.lse[static_cast<long long>(q0 + token) * p.a.Hq + hk * G + g];
+                    const float e = p.lse[t * p.a.Hq + h];
                     neg_lse = e == -INFINITY ? e : -e * kLog2e;
                 }
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    float x[8], y[8];
-                    unpack8(o[i], x);
-                    unpack8(d[i], y);
+                for (int u = 0; u < V; ++u) {
+                    float a[8], b[8];
+                    unpack8(o[u], a);
+                    unpack8(d[u], b);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) delta += x[e] * y[e];
+                    for (int e = 0; e < 8; ++e) delta += a[e] * b[e];
                 }
-            }
-            part_delta[grp * 128 + row] = delta;
-            bar_sync(1, kCompute * 32);
-            delta = part_delta[row];
+                part_delta[grp * 128 + row] = delta;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(delta_bar);
+                warp_wait(delta_bar, had & 1, abort_flag);
+                delta = part_delta[row];
 #pragma unroll
-            for (int i = 1; i < kGroups; ++i) delta += part_delta[i * 128 + row];
+                for (int u = 1; u < kGroups; ++u) delta += part_delta[u * 128 + row];
+            }
             const float neg_delta = -delta;
             if (valid && grp == 0) {
-                const long long at = (static_cast<long long>(hk) * p.s.Tq + q0 + token) * G + g;
+                const long long at = (static_cast<long long>(it.hk) * p.s.Tq + t) * G + head;
                 p.row_lse[at] = neg_lse;
                 p.row_delta[at] = neg_delta;
             }
-            for (int j = 0; j < n; ++j) {
-                warp_wait(s_bar, j & 1, abort_flag);
+            for (int j = 0; j < n; ++j, ++g) {
+                warp_wait(s_bar, g & 1, abort_flag);
                 tc_fence_after();
                 float s[kCols], d[kCols];
                 load_cols(lanes + TM_S + kCols * grp, s);
                 warp_arrive(s_read, lane);
 #pragma unroll
-                for (int i = 0; i < kCols; i += 2) {
-                    fma2v(s[i], s[i + 1], c, neg_lse, neg_lse);
-                    s[i] = exp2_fast(s[i]);
-                    s[i + 1] = exp2_fast(s[i + 1]);
+                for (int e = 0; e < kCols; e += 2) {
+                    fma2v(s[e], s[e + 1], c, neg_lse, neg_lse);
+                    s[e] = exp2_fast(s[e]);
+                    s[e + 1] = exp2_fast(s[e + 1]);
                 }
-                warp_wait(dp_bar(j & 1), (j >> 1) & 1, abort_flag);
+                warp_wait(dp_bar(g & 1), (g >> 1) & 1, abort_flag);
                 tc_fence_after();
-                const uint32_t tD = lanes + TM_DP + 128 * (j & 1) + kCols * grp;
+                const uint32_t tD = lanes + TM_DP + 128 * (g & 1) + kCols * grp;
                 load_cols(tD, d);
 #pragma unroll
-                for (int i = 0; i < kCols; i += 2) {
-                    add2(d[i], d[i + 1], neg_delta, neg_delta);
-                    mul2(d[i], d[i + 1], s[i], s[i + 1]);
+                for (int e = 0; e < kCols; e += 2) {
+                    add2(d[e], d[e + 1], neg_delta, neg_delta);
+                    mul2(d[e], d[e + 1], s[e], s[e + 1]);
                 }
                 if ((j + 1) * kRows > open) {
                     const int lim = mine - j * kRows - kCols * grp;
 #pragma unroll
-                    for (int i = 0; i < kCols; ++i) d[i] = i < lim ? d[i] : 0.f;
+                    for (int e = 0; e < kCols; ++e) d[e] = e < lim ? d[e] : 0.f;
                 }
                 store_cols(tD, d);
-                warp_arrive(ds_bar, lane);
+                warp_arrive(ds_bar(g & 1), lane);
             }
-            if (n > 0) warp_wait(done_bar, 0, abort_flag);
-            {
+            if (n > 0) {
+                warp_wait(dq_bar, had & 1, abort_flag);
+                ++had;
                 tc_fence_after();
-                constexpr int W = DP / kGroups;
-                store_rows<W>(lanes + TM_DQ + grp * W, n > 0, p.scale, smem + warp * 32 * W * 2, lane,
-                              valid ? p.dq.row(q0 + token, hk * G + g) : nullptr, grp * W, p.a.D);
+            }
+            bf16* dst = p.dq.row(t, h);
+#pragma unroll
+            for (int q = 0; q < W; q += 16) {
+                uint32_t o[16];
+                if (n > 0) {
+                    tmem_ld16(lanes + TM_DQ + grp * W + q, o);
+                    tmem_ld_wait();
+                    if (q + 16 == W) warp_arrive(dq_free, lane);
+                }
+#pragma unroll
+                for (int u = 0; u < 16; u += 8) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = n > 0 ? __uint_as_float(o[u + e]) * p.scale : 0.f;
+                    if (valid && grp * W + q + u < p.a.D)
+                        *reinterpret_cast<uint4*>(dst + grp * W + q + u) = pack8(v);
+                }
             }
         }
     }
@@ -586,7 +671,7 @@ cudaError_t backward(const Attention& p, cudaStream_t st) {
     const int G = p.a.Hq / p.a.Hkv, D = p.a.D, tpt = kRows / G;
     float* second = p.delta + static_cast<size_t>(p.s.Tq) * p.a.Hq;
     const Params prm{p.a, p.s, p.scale, p.out, p.dout, p.dq, p.dk, p.dv, p.lse, p.delta, second,
-                     p.err, tpt};
+                     p.err, tpt, static_cast<int>(tile_bound(p.s.Tq, p.s.B, p.s.max_q, tpt))};
     CUtensorMap mq, md, mk, mv;
     if (p.s.Tq > 0 && (!make_tmap_heads(&mq, p.q, p.s.Tq, p.a.Hq, D, G, tpt) ||
                        !make_tmap_heads(&md, p.dout, p.s.Tq, p.a.Hq, D, G, tpt)))
@@ -597,14 +682,14 @@ cudaError_t backward(const Attention& p, cudaStream_t st) {
     // without queries or without keys no tile is loaded
     if (p.s.Tq == 0) mq = md = mk;
     if (p.s.Tk == 0) mk = mv = mq;
-    const long long qi = tile_bound(p.s.Tq, p.s.B, p.s.max_q, tpt);
-    if (p.s.Tq > 0 && qi > 0) {
+    const long long items = static_cast<long long>(prm.items) * p.a.Hkv;
+    if (p.s.Tq > 0 && items > 0) {
         auto kfn = dq_kernel<DP>;
         cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              C::SMEM_Q);
         if (e != cudaSuccess) return e;
         LaunchScope ls("attention_dq", st);
-        e = launch_pdl(kfn, dim3(static_cast<unsigned>(qi * p.a.Hkv)), dim3(kThreads), C::SMEM_Q, st,
+        e = launch_pdl(kfn, dim3(static_cast<unsigned>(std::min<long long>(items, num_sms()))), dim3(kThreads), C::SMEM_Q, st,
                      mq, md, mk, mv, prm);
         if (e != cudaSuccess) return e;
     }

@@ -107,20 +107,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// Named barrier over `n` threads, and one that also ORs a predicate.
-__device__ __forceinline__ void bar_sync(int id, int n) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
-}
-__device__ __forceinline__ bool bar_or(int id, int n, bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-        "bar.red.or.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)
-        : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(n)
-        : "memory");
-    return r != 0;
-}
 // One arrival for a warp whose lanes' earlier TMEM accesses are waited for.
 __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
     tc_fence_before();
