@@ -153,7 +153,12 @@ AT = [  # lens_q, lens_k, Hq, Hkv, D, causal
     ([64, 10], [0, 7], 4, 4, 128, False), ([33, 70], [300, 5], 8, 1, 40, False),
     ([513], None, 5, 1, 128, True), ([200, 100], None, 16, 1, 64, True),
     ([90], [1000], 10, 2, 128, True), ([700], None, 2, 2, 64, False),
-    ([3, 2], [200, 131], 64, 1, 24, True), ([1024], None, 4, 1, 128, True)]
+    ([3, 2], [200, 131], 64, 1, 24, True), ([1024], None, 4, 1, 128, True),
+    # more items of work than SMs, and more sequences than one warp holds
+    ([(7 * i) % 41 for i in range(70)], None, 8, 4, 64, True),
+    ([(11 * i) % 150 for i in range(33)], [(13 * i) % 160 for i in range(33)], 6, 6, 40, True),
+    ([(5 * i) % 140 + 1 for i in range(32)], [(17 * i) % 300 for i in range(32)], 9, 3, 72, False),
+    ([600, 20, 900, 1, 300], None, 16, 4, 128, True)]
 
 
 def attention_data(case, seed=0, std=1.0):
@@ -281,6 +286,22 @@ def test_non_finite_values_stay_in_their_sequence():
             assert torch.equal(x[:a], y[:a]) and torch.equal(x[b:], y[b:])
             assert (y[T:] == 0).all()
         del clean
+
+
+def test_calls_back_to_back_give_the_same_bits():
+    """Hundreds of forward and backward passes in a row, without a wait between them: no
+    bounded wait runs out and the last results are the first ones."""
+    case = ([700, 64, 333], None, 12, 4, 128, True)
+    att, lq, lk, q, k, v, do = attention_data(case, 17)
+    cq = offsets(lq)
+    out, lse = att.forward(q, k, v, cq, 700)
+    grads = att.backward(do, q, k, v, out, lse, cq, 700)
+    first = [x.clone() for x in (out, lse) + grads]
+    for _ in range(400):
+        att.forward(q, k, v, cq, 700, out=out, lse=lse)
+        att.backward(do, q, k, v, out, lse, cq, 700, dq=grads[0], dk=grads[1], dv=grads[2])
+    for a, b in zip(first, (out, lse) + grads):
+        assert torch.equal(a, b)
 
 
 def test_gradient_is_the_difference():
@@ -440,3 +461,15 @@ def test_wrong_tensors_are_refused():
         att.forward(q, k, v, cq.long(), 8)
     with pytest.raises(B.MoeError):
         att.decode(q, v[None].contiguous(), v[None].contiguous(), cq[None], cq[:1], 8)
+
+
+def test_decoder_block_example():
+    """The example runs: one training step, then served tokens that agree with it."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "decoder_block.py")
+    spec = importlib.util.spec_from_file_location("decoder_block", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    assert m.main() < 1e-2
