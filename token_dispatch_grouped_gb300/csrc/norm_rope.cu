@@ -20,6 +20,7 @@
 // operations an instruction. (One weight load and one fp32 shuffle a value, at half the
 // warps: 34.8 us for 4096 tokens of 32/8 heads of 128 against XXX.)
 #include "attn.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 namespace attn {
@@ -289,12 +290,19 @@ norm_rope_kernel(const NormRope p, const Runs rn) {
 // and q = sum dy w x: dx = r dy w - x r^3 q / D, dw += r dy x. A warp walks (token, run)
 // tasks of the queries, then of the keys, with the grid's stride, and keeps its piece of
 // that weight gradient in registers; a CTA adds its warps' sums in warp order and writes
-// one partial row [2][D].
+// one partial row [2][D]. The rows come through a ring in shared memory that each lane
+// fills (cp.async) and reads for itself, kAhead batches ahead: the registers that the
+// sums take leave 16 warps an SM, too few to hide the loads by themselves (62 us for 16384
+// tokens of 16/4 heads of 128 without the ring, against XXX).
+constexpr int kBatch = 2;  // row groups of a batch
+constexpr int kAhead = 4;  // slots of the ring
+constexpr int kRing = kWarps * kAhead * kBatch * 2 * 512;
+
 template <int LPR, int SWAP>
 __global__ void __launch_bounds__(kWarps * 32, 2)
 norm_rope_backward_kernel(const NormRope p, Heads dq_out, Heads dk_out, float* part, const Runs rn) {
-    constexpr int RPW = 32 / LPR;
-    constexpr int U = 2;  // two rows' x and g in flight per lane
+    constexpr int RPW = 32 / LPR, U = kBatch;
+    extern __shared__ __align__(16) uint8_t s_ring[];  // [warp][slot][group][x, g][lane]
     __shared__ __align__(16) bf16 s_buf[SWAP == SWAP_ROW ? kWarps * RPW * 128 : 8];
     __shared__ float s_dw[kWarps][2][128];
     pdl_wait();
@@ -306,8 +314,10 @@ norm_rope_backward_kernel(const NormRope p, Heads dq_out, Heads dk_out, float* p
     const bool live = piece * 8 < D;
     const bool norm = p.wq != nullptr;
     bf16* buf = s_buf + (SWAP == SWAP_ROW ? (warp * RPW + sub) * 128 : 0);
+    uint4* ring = reinterpret_cast<uint4*>(s_ring) + warp * (kAhead * U * 2 * 32) + lane;
     const float inv_d = 1.f / static_cast<float>(D);
     const long long step = static_cast<long long>(gridDim.x) * kWarps;
+    const long long start = static_cast<long long>(blockIdx.x) * kWarps + warp;
 #pragma unroll 1
     for (int kind = 0; kind < 2; ++kind) {
         float acc[8], w[8];
@@ -318,42 +328,80 @@ norm_rope_backward_kernel(const NormRope p, Heads dq_out, Heads dk_out, float* p
         }
         const Heads xs = kind == 0 ? p.q : p.k, gs = kind == 0 ? dq_out : dk_out;
         const Heads os = kind == 0 ? p.q_out : p.k_out;
-        const int runs = kind == 0 ? rn.q : rn.k, rows = kind == 0 ? p.a.Hq : p.a.Hkv;
-        const long long tasks = static_cast<long long>(p.T) * runs;
-        for (long long task = static_cast<long long>(blockIdx.x) * kWarps + warp; task < tasks;
-             task += step) {
-            const int t = static_cast<int>(task / runs);
-            const int r0 = static_cast<int>(task % runs) * rn.rows, r1 = min(rows, r0 + rn.rows);
-            const bf16* xr = xs.row(t, r0 + sub) + piece * 8;
-            const bf16* gr = gs.row(t, r0 + sub) + piece * 8;
-            bf16* orow = os.row(t, r0 + sub) + piece * 8;
-            uint4 xin[U], gin[U];
-            const auto load = [&](int rb) {
+        const int runs = max(1, kind == 0 ? rn.q : rn.k);
+        const int rows = kind == 0 ? p.a.Hq : p.k.p ? p.a.Hkv : 0;
+        const int step_t = static_cast<int>(step / runs), step_r = static_cast<int>(step % runs);
+        // A batch of this warp: rows rb .. of run `run` of token t.
+        struct At {
+            int t, run, rb;
+        };
+        const auto next_task = [&](At& a) {
+            a.t += step_t;
+            a.run += step_r;
+            if (a.run >= runs) {
+                a.run -= runs;
+                ++a.t;
+            }
+            a.rb = a.run * rn.rows;
+        };
+        const auto last_row = [&](const At& a) { return min(rows, (a.run + 1) * rn.rows); };
+        At in{static_cast<int>(start / runs), static_cast<int>(start % runs), 0};
+        in.rb = in.run * rn.rows;
+        if (rows == 0) in.t = p.T;
+        At at = in;
+        int slot_in = 0, slot = 0;
+        const auto issue = [&]() {  // the next batch into the ring (empty past the last)
+            if (in.t < p.T) {
+                const int r1 = last_row(in);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int r = in.rb + u * RPW + sub;
+                    if (r < r1 && live) {
+                        uint4* dst = ring + (slot_in * U + u) * 64;
+                        ptx::cp_async16(ptx::smem_u32(dst), xs.row(in.t, r) + piece * 8, 16);
+                        ptx::cp_async16(ptx::smem_u32(dst + 32), gs.row(in.t, r) + piece * 8, 16);
+                    }
+                }
+                in.rb += RPW * U;
+                if (in.rb >= r1) next_task(in);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            slot_in = slot_in + 1 == kAhead ? 0 : slot_in + 1;
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead - 1; ++i) issue();
+        int pos = 0;
+        if (SWAP != SWAP_NONE && at.t < p.T) pos = p.positions[at.t];
+        while (at.t < p.T) {
+            const At task = at;
+            const int r1 = last_row(at);
+            next_task(at);
+            const int pos_now = pos;
+            float c[8], s[8];
+            bool bad = false;
+            if constexpr (SWAP != SWAP_NONE) {
+                if (at.t < p.T) pos = p.positions[at.t];  // of the next task
+                bad = pos_now < 0 || pos_now >= p.table_rows;
+                if (bad && lane == 0) raise_error(p.err, MOE_ERR_BAD_INDEX);
+                load_rotation<SWAP>(p.table + static_cast<long long>(bad ? 0 : pos_now) * (p.rot >> 1),
+                                    p.rot, p.interleaved, piece, c, s);
+            }
+            bf16* orow = os.row(task.t, task.rb + sub) + piece * 8;
+            for (int rb = task.rb; rb < r1; rb += RPW * U) {
+                issue();
+                asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+                uint4 xin[U], gin[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     xin[u] = gin[u] = make_uint4(0u, 0u, 0u, 0u);
                     if (rb + u * RPW + sub < r1 && live) {
-                        xin[u] = *reinterpret_cast<const uint4*>(xr + (rb - r0 + u * RPW) * xs.hs);
-                        gin[u] = *reinterpret_cast<const uint4*>(gr + (rb - r0 + u * RPW) * gs.hs);
+                        xin[u] = ring[(slot * U + u) * 64];
+                        gin[u] = ring[(slot * U + u) * 64 + 32];
                     }
                 }
-            };
-            load(r0);
-            float c[8], s[8];
-            if constexpr (SWAP != SWAP_NONE) {
-                const int pos = p.positions[t];
-                if (pos < 0 || pos >= p.table_rows) {
-                    if (lane == 0) raise_error(p.err, MOE_ERR_BAD_INDEX);
-                    continue;
-                }
-                load_rotation<SWAP>(p.table + static_cast<long long>(pos) * (p.rot >> 1), p.rot,
-                                    p.interleaved, piece, c, s);
-            }
-            for (int rb = r0; rb < r1; rb += RPW * U) {
-                if (rb > r0) load(rb);
+                slot = slot + 1 == kAhead ? 0 : slot + 1;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    if (rb + u * RPW >= r1) break;  // the same for the whole warp
                     float x[8], dy[8];
                     unpack8(xin[u], x);
                     unpack8(gin[u], dy);
@@ -366,6 +414,7 @@ norm_rope_backward_kernel(const NormRope p, Heads dq_out, Heads dk_out, float* p
                             fma2(dy[e], dy[e + 1], o[e], o[e + 1], -s[e], -s[e + 1]);
                         }
                     }
+                    const bool mine = rb + u * RPW + sub < r1 && !bad;
                     if (norm) {
                         float s0 = 0.f, s1 = 0.f, q0 = 0.f, q1 = 0.f, g[8];
 #pragma unroll
@@ -376,23 +425,25 @@ norm_rope_backward_kernel(const NormRope p, Heads dq_out, Heads dk_out, float* p
                             mul2(g[e], g[e + 1], x[e], x[e + 1]);           // dy x
                             fma2(q0, q1, g[e], g[e + 1], w[e], w[e + 1]);
                         }
-                        // rows past the run are zeros and add nothing
+                        // rows past the run (zeros) and rows left out add nothing
                         float rr = rsqrtf(row_sum<LPR>(s0 + s1) * inv_d + p.eps);
-                        if (rb + u * RPW + sub >= r1) rr = 0.f;
                         const float k = -rr * rr * rr * (row_sum<LPR>(q0 + q1) * inv_d);
+                        if (mine) {
 #pragma unroll
-                        for (int e = 0; e < 8; e += 2) {
-                            fma2(acc[e], acc[e + 1], g[e], g[e + 1], rr, rr);
-                            mul2(dy[e], dy[e + 1], w[e], w[e + 1]);
-                            mul2(dy[e], dy[e + 1], rr, rr);
-                            fma2(dy[e], dy[e + 1], x[e], x[e + 1], k, k);
+                            for (int e = 0; e < 8; e += 2) {
+                                fma2(acc[e], acc[e + 1], g[e], g[e + 1], rr, rr);
+                                mul2(dy[e], dy[e + 1], w[e], w[e + 1]);
+                                mul2(dy[e], dy[e + 1], rr, rr);
+                                fma2(dy[e], dy[e + 1], x[e], x[e + 1], k, k);
+                            }
                         }
                     }
-                    if (rb + u * RPW + sub < r1 && live)
-                        *reinterpret_cast<uint4*>(orow + (rb - r0 + u * RPW) * os.hs) = pack8(dy);
+                    if (mine && live)
+                        *reinterpret_cast<uint4*>(orow + (rb - task.rb + u * RPW) * os.hs) = pack8(dy);
                 }
             }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
 #pragma unroll
@@ -482,10 +533,13 @@ cudaError_t fwd(const NormRope& p, bool append, cudaStream_t st) {
 
 template <int LPR, int SWAP>
 cudaError_t bwd(const NormRope& p, Heads dq_out, Heads dk_out, float* part, cudaStream_t st) {
-    const Runs r = plan_runs(p, 32 / LPR, 2, false);
+    const Runs r = plan_runs(p, 32 / LPR, 4, false);
+    auto kfn = norm_rope_backward_kernel<LPR, SWAP>;
+    const cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+    if (e != cudaSuccess) return e;
     LaunchScope ls("norm_rope_backward", st);
-    return launch_k(norm_rope_backward_kernel<LPR, SWAP>, dim3(norm_rope_parts(p.a, p.T)),
-                    dim3(kWarps * 32), 0, st, p, dq_out, dk_out, part, r);
+    return launch_k(kfn, dim3(norm_rope_parts(p.a, p.T)), dim3(kWarps * 32), kRing, st, p, dq_out,
+                    dk_out, part, r);
 }
 
 }  // namespace
