@@ -120,8 +120,8 @@ int moe_attention_forward(moe_attn_shape a, moe_packed s, float scale, moe_heads
                           moe_heads v, moe_heads out, float* lse, void* stream);
 
 /* Gradients of moe_attention_forward from dout and its inputs and outputs. With
- * P = exp(scale q k^T - lse), delta = sum_i dout_i out_i, dP = dout v^T and
- * dS = P (dP - delta): dv = P^T dout, dq = scale dS k, dk = scale dS^T q, where dk
+ * P = exp(scale q k^T - lse), dP = dout v^T, delta = sum_j P_j dP_j = sum_i dout_i out_i
+ * and dS = P (dP - delta): dv = P^T dout, dq = scale dS k, dk = scale dS^T q, where dk
  * and dv sum over the G query heads of their head. Written, not accumulated; a
  * non-finite value of a sequence reaches no other sequence. */
 size_t moe_attention_backward_workspace_size(moe_attn_shape a, moe_packed s);

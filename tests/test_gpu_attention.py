@@ -62,7 +62,8 @@ NR = [  # T, Hq, Hkv, D, rot, layout, norm
     (33, 5, 1, 80, 40, "half", True), (33, 5, 1, 80, 80, "interleaved", True),
     (7, 3, 3, 128, 128, "half", False), (7, 3, 1, 40, 0, "half", True),
     (130, 32, 8, 128, 128, "half", True), (900, 4, 4, 16, 6, "half", True),
-    (9, 12, 4, 120, 2, "interleaved", False), (6000, 2, 1, 128, 64, "half", True)]
+    (9, 12, 4, 120, 2, "interleaved", False), (6000, 2, 1, 128, 64, "half", True),
+    (20001, 2, 2, 16, 16, "half", True), (19999, 3, 1, 24, 8, "interleaved", True)]
 
 
 def norm_rope_data(case, seed=0, fused=True):

@@ -14,7 +14,7 @@
 // 128-key tile of K and V from shared memory. Roles:
 //   warp 10    finds the next item while the others work on the last one (a CTA per item
 //              spent 7.6 us outside its steps: 53 us for the packed batch of 4096 tokens
-//              against XXX);
+//              against 45);
 //   warp 9     loads: Q, then K and V tiles by TMA, into the next item as tiles fall free;
 //   warp 8     the tensor cores: S_x = Q_x K^T (both from shared memory) into TMEM,
 //              O_x += P_x V with P_x as the TMEM operand;

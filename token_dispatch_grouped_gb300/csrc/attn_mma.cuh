@@ -225,9 +225,9 @@ __device__ __forceinline__ int key_items(const Packed& s, const Work& w, int til
 
 // Work item `want` of the batch, by one warp. Sequences that are not valid have none.
 // Up to 32 sequences (one a lane) the items with the most steps come first, over all of
-// them: the number of steps at rank `want` is found by bisection, then the sequence. (In
-// sequence order a long sequence at the batch's end starts last: XXX.) Beyond, the items
-// of a sequence follow each other, most steps first.
+// them, so that the shortest end the launch: the number of steps at rank `want` is found by
+// bisection, then the sequence. Beyond, the items of a sequence follow each other, most
+// steps first.
 template <bool KEYS>
 __device__ __forceinline__ Work find_work(const Packed& s, int tile, int want, int lane, int* err) {
     const int size = KEYS ? kRows : tile;

@@ -18,7 +18,7 @@
 // lane's own registers (interleaved), by shuffles (half layout, when whole pieces swap), or
 // through shared memory (any other number of rotated dims). Arithmetic is two fp32
 // operations an instruction. (One weight load and one fp32 shuffle a value, at half the
-// warps: 34.8 us for 4096 tokens of 32/8 heads of 128 against XXX.)
+// warps: 34.8 us for 4096 tokens of 32/8 heads of 128 against 19.)
 #include "attn.cuh"
 #include "ptx.cuh"
 
@@ -148,8 +148,9 @@ struct Runs {
     int total() const { return q + k + v; }
 };
 
-// U: row loads in flight per lane. A block takes one run of kWarps tokens.
-template <int LPR, int SWAP, bool APPEND, int U>
+// U: row loads in flight per lane; NT: tokens that a warp takes, one after the other. A block
+// takes one run of kWarps * NT tokens.
+template <int LPR, int SWAP, bool APPEND, int U, int NT>
 __global__ void __launch_bounds__(kWarps * 32, U == 2 ? 4 : 3)
 norm_rope_kernel(const NormRope p, const Runs rn) {
     constexpr int RPW = 32 / LPR;  // rows of a warp at once
@@ -157,8 +158,8 @@ norm_rope_kernel(const NormRope p, const Runs rn) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int t = blockIdx.x * kWarps + warp;
-    if (t >= p.T) return;
+    const int t0 = (blockIdx.x * kWarps + warp) * NT;
+    if (t0 >= p.T) return;
     int run = blockIdx.y, kind = 0;  // 0 queries, 1 keys, 2 values
     if (run >= rn.q) {
         run -= rn.q;
@@ -173,22 +174,23 @@ norm_rope_kernel(const NormRope p, const Runs rn) {
     const int r0 = run * rn.rows, r1 = min(kind == 0 ? p.a.Hq : Hkv, r0 + rn.rows);
     const bool live = piece * 8 < D;
     const Heads src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-    const bf16* in_row = src.row(t, r0 + sub) + piece * 8;
+    const bf16* in_row = src.row(t0, r0 + sub) + piece * 8;
 
     uint4 in[U];
-    const auto load = [&](int rb) {
+    const auto load = [&](const bf16* row, int rb) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             in[u] = make_uint4(0u, 0u, 0u, 0u);
             if (rb + u * RPW + sub < r1 && live)
-                in[u] = *reinterpret_cast<const uint4*>(in_row + (rb - r0 + u * RPW) * src.hs);
+                in[u] = *reinterpret_cast<const uint4*>(row + (rb - r0 + u * RPW) * src.hs);
         }
     };
     // what does not depend on another load comes first, all of it in flight at once
-    load(r0);
+    load(in_row, r0);
     const bool skip = has_error(p.err);
-    const int pos = SWAP != SWAP_NONE && kind < 2 ? p.positions[t] : 0;
-    const long long slot = APPEND && kind > 0 ? p.slots[t] : 0;
+    int positions = 0;  // lane i: of token t0 + i
+    if (SWAP != SWAP_NONE && kind < 2 && lane < NT && t0 + lane < p.T) positions = p.positions[t0 + lane];
+    const long long slot = APPEND && kind > 0 ? p.slots[t0] : 0;
     const bool norm = p.wq != nullptr;
     float w[8], wp[8];  // the weights of this lane's values and of their partners
     if (norm && kind < 2) {
@@ -206,9 +208,11 @@ norm_rope_kernel(const NormRope p, const Runs rn) {
     if (skip) return;
 
     // where the rows go
-    bf16* out = (kind == 0 ? p.q_out : p.k_out).row(t, r0 + sub) + piece * 8;
+    bf16* out = (kind == 0 ? p.q_out : p.k_out).row(t0, r0 + sub) + piece * 8;
+    const long long out_ts = (kind == 0 ? p.q_out : p.k_out).ts;
     long long out_hs = (kind == 0 ? p.q_out : p.k_out).hs;
     if constexpr (APPEND) {
+        static_assert(NT == 1, "a slot per task");
         if (kind > 0) {
             if (slot >= (static_cast<long long>(p.pages) << p.page_shift)) {
                 if (lane == 0) raise_error(p.err, MOE_ERR_BAD_INDEX);
@@ -222,7 +226,7 @@ norm_rope_kernel(const NormRope p, const Runs rn) {
         }
         if (kind == 2) {
             for (int rb = r0; rb < r1; rb += RPW * U) {
-                if (rb > r0) load(rb);
+                if (rb > r0) load(in_row, rb);
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (rb + u * RPW + sub < r1 && live)
@@ -231,58 +235,69 @@ norm_rope_kernel(const NormRope p, const Runs rn) {
             return;
         }
     }
-    float a[8], b[8];  // A and B
-    if constexpr (SWAP != SWAP_NONE) {
-        if (pos < 0 || pos >= p.table_rows) {  // the whole warp: one token
-            if (lane == 0) raise_error(p.err, MOE_ERR_BAD_INDEX);
-            return;
-        }
-        load_rotation<SWAP>(p.table + static_cast<long long>(pos) * (p.rot >> 1), p.rot,
-                            p.interleaved, piece, a, b);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] = 1.f;
-    }
-    if (norm) {
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            mul2(a[e], a[e + 1], w[e], w[e + 1]);
-            if constexpr (SWAP == SWAP_OWN) mul2(b[e], b[e + 1], w[e + 1], w[e]);
-            if constexpr (SWAP == SWAP_LANE || SWAP == SWAP_ROW) mul2(b[e], b[e + 1], wp[e], wp[e + 1]);
-        }
-    }
     bf16* buf = s_buf + (SWAP == SWAP_ROW ? (warp * RPW + sub) * 128 : 0);
     const float inv_d = 1.f / static_cast<float>(D);
-
-    for (int rb = r0; rb < r1; rb += RPW * U) {
-        if (rb > r0) load(rb);
+#pragma unroll 1
+    for (int i = 0; i < NT && t0 + i < p.T; ++i) {
+        float a[8], b[8];  // A and B
+        bool bad = false;
+        if constexpr (SWAP != SWAP_NONE) {
+            const int pos = __shfl_sync(0xffffffffu, positions, i);
+            bad = pos < 0 || pos >= p.table_rows;  // the whole warp: one token
+            if (bad && lane == 0) raise_error(p.err, MOE_ERR_BAD_INDEX);
+            load_rotation<SWAP>(p.table + static_cast<long long>(bad ? 0 : pos) * (p.rot >> 1), p.rot,
+                                p.interleaved, piece, a, b);
+        } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (rb + u * RPW >= r1) break;  // the same for the whole warp
-            float x[8], y[8];
-            unpack8(in[u], x);
-            float rr = 1.f;
-            if (norm) {
-                float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) fma2(s0, s1, x[e], x[e + 1], x[e], x[e + 1]);
-                rr = rsqrtf(row_sum<LPR>(s0 + s1) * inv_d + p.eps);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = x[e];
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) mul2(y[e], y[e + 1], a[e], a[e + 1]);
-            if constexpr (SWAP != SWAP_NONE) {
-                float o[8];
-                partners<LPR, SWAP>(in[u], x, p.rot, p.interleaved, piece, buf, o);
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) fma2(y[e], y[e + 1], o[e], o[e + 1], b[e], b[e + 1]);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) mul2(y[e], y[e + 1], rr, rr);
-            if (rb + u * RPW + sub < r1 && live)
-                *reinterpret_cast<uint4*>(out + (rb - r0 + u * RPW) * out_hs) = pack8(y);
+            for (int e = 0; e < 8; ++e) a[e] = 1.f;
         }
+        if (norm) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                mul2(a[e], a[e + 1], w[e], w[e + 1]);
+                if constexpr (SWAP == SWAP_OWN) mul2(b[e], b[e + 1], w[e + 1], w[e]);
+                if constexpr (SWAP == SWAP_LANE || SWAP == SWAP_ROW)
+                    mul2(b[e], b[e + 1], wp[e], wp[e + 1]);
+            }
+        }
+        for (int rb = r0; rb < r1; rb += RPW * U) {
+            if (rb > r0) load(in_row, rb);
+            uint4 rows[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) rows[u] = in[u];
+            if (NT > 1 && rb + RPW * U >= r1 && i + 1 < NT && t0 + i + 1 < p.T) {
+                in_row += src.ts;  // the next token's first rows
+                load(in_row, r0);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float x[8], y[8];
+                unpack8(rows[u], x);
+                float rr = 1.f;
+                if (norm) {
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) fma2(s0, s1, x[e], x[e + 1], x[e], x[e + 1]);
+                    rr = rsqrtf(row_sum<LPR>(s0 + s1) * inv_d + p.eps);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = x[e];
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) mul2(y[e], y[e + 1], a[e], a[e + 1]);
+                if constexpr (SWAP != SWAP_NONE) {
+                    float o[8];
+                    partners<LPR, SWAP>(rows[u], x, p.rot, p.interleaved, piece, buf, o);
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2)
+                        fma2(y[e], y[e + 1], o[e], o[e + 1], b[e], b[e + 1]);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) mul2(y[e], y[e + 1], rr, rr);
+                if (rb + u * RPW + sub < r1 && live && !bad)
+                    *reinterpret_cast<uint4*>(out + (rb - r0 + u * RPW) * out_hs) = pack8(y);
+            }
+        }
+        out += out_ts;
     }
 }
 
@@ -293,7 +308,7 @@ norm_rope_kernel(const NormRope p, const Runs rn) {
 // one partial row [2][D]. The rows come through a ring in shared memory that each lane
 // fills (cp.async) and reads for itself, kAhead batches ahead: the registers that the
 // sums take leave 16 warps an SM, too few to hide the loads by themselves (62 us for 16384
-// tokens of 16/4 heads of 128 without the ring, against XXX).
+// tokens of 16/4 heads of 128 without the ring, against 52).
 constexpr int kBatch = 2;  // row groups of a batch
 constexpr int kAhead = 4;  // slots of the ring
 constexpr int kRing = kWarps * kAhead * kBatch * 2 * 512;
@@ -512,14 +527,17 @@ Runs plan_runs(const NormRope& p, int rpw, int batch, bool append) {
     }
 }
 
-template <int LPR, int SWAP, bool APPEND, int U>
+template <int LPR, int SWAP, bool APPEND, int U, int NT>
 cudaError_t fwd_u(const NormRope& p, const Runs& r, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>((p.T + kWarps - 1) / kWarps), r.total());
-    return launch_k(norm_rope_kernel<LPR, SWAP, APPEND, U>, grid, dim3(kWarps * 32), 0, st, p, r);
+    constexpr int TOKENS = kWarps * NT;
+    const dim3 grid(static_cast<unsigned>((p.T + TOKENS - 1) / TOKENS), r.total());
+    return launch_k(norm_rope_kernel<LPR, SWAP, APPEND, U, NT>, grid, dim3(kWarps * 32), 0, st, p, r);
 }
 
-// Two loads in flight per lane where a token's heads are no more than that (fewer
-// registers, so more warps: XXX), else four.
+// Two loads in flight per lane where a token's heads of a kind are no more than that (fewer
+// registers, so more warps), else four; and several tokens a warp where there are so many
+// tokens that they fill the GPU all the same (65536 tokens of 8/8 heads of 64: 88 us with
+// four loads and one token, 72 with two and one, 56 with two and four).
 template <int LPR, int SWAP>
 cudaError_t fwd(const NormRope& p, bool append, cudaStream_t st) {
     constexpr int RPW = 32 / LPR;
@@ -527,8 +545,11 @@ cudaError_t fwd(const NormRope& p, bool append, cudaStream_t st) {
     const bool few = p.a.Hq <= 2 * RPW || r.rows <= 2 * RPW;
     LaunchScope ls(append ? "kv_append" : "norm_rope", st);
     if (append)
-        return few ? fwd_u<LPR, SWAP, true, 2>(p, r, st) : fwd_u<LPR, SWAP, true, 4>(p, r, st);
-    return few ? fwd_u<LPR, SWAP, false, 2>(p, r, st) : fwd_u<LPR, SWAP, false, 4>(p, r, st);
+        return few ? fwd_u<LPR, SWAP, true, 2, 1>(p, r, st) : fwd_u<LPR, SWAP, true, 4, 1>(p, r, st);
+    if (!few) return fwd_u<LPR, SWAP, false, 4, 1>(p, r, st);
+    return static_cast<long long>(p.T) * r.total() >= num_sms() * 32ll * 8
+               ? fwd_u<LPR, SWAP, false, 2, 4>(p, r, st)
+               : fwd_u<LPR, SWAP, false, 2, 1>(p, r, st);
 }
 
 template <int LPR, int SWAP>
