@@ -30,6 +30,8 @@
  *     bf16. Where a product runs on the tensor cores, the softmax weights and
  *     their gradients are its bf16 operands. Every result is the same from run to
  *     run (no floating-point atomics).
+ *   - The attention kernels use programmatic stream serialization as the grouped
+ *     GEMMs do (MOE_PDL); stream order holds as for ordinary launches.
  */
 #ifndef MOE_ATTENTION_GB300_H
 #define MOE_ATTENTION_GB300_H
