@@ -214,3 +214,25 @@ def test_frequencies():
         rope_inv_freq(64, scaling="other")
     with pytest.raises(ValueError):
         rope_inv_freq(63)
+
+
+def test_integers_off_their_alignment_are_refused(B):
+    """int32 arrays are read as words: an address that is no multiple of 4 is refused on
+    the host, before any launch."""
+    mis, a = B.MOE_ERR_MISALIGNED, B.MoeAttnShape(4, 2, 64)
+    q, k = _heads(B, 256, 64), _heads(B, 128, 64)
+    rope, cache = B.MoeRope(FAKE, 10, 64, 0), B.MoeKvCache(FAKE, FAKE, 5, 16)
+    for off in (1, 2, 3):
+        at = FAKE + off
+        assert _norm_rope(B, pos=at) == mis
+        assert B.LIB.moe_norm_rope_backward(a, 3, q, k, q, k, FAKE, FAKE, 1e-6, at, rope, q, k,
+                                            FAKE, FAKE, FAKE, 1 << 24, None) == mis
+        assert B.LIB.moe_kv_append(a, 3, q, k, k, FAKE, FAKE, 1e-6, at, rope, FAKE, q, cache,
+                                   None) == mis
+        for s in (B.MoePacked(2, 10, 10, 8, 8, 1, at, FAKE), B.MoePacked(2, 10, 10, 8, 8, 1, FAKE, at)):
+            assert B.LIB.moe_attention_forward(a, s, 0.125, q, k, k, q, FAKE, None) == mis
+            assert B.LIB.moe_attention_backward(a, s, 0.125, q, q, k, k, q, FAKE, q, k, k, FAKE,
+                                                1 << 20, None) == mis
+        for table, lens in ((at, FAKE), (FAKE, at)):
+            assert B.LIB.moe_attention_decode(a, 2, 1, 60, 0.125, q, cache, table, 4, lens, q, FAKE,
+                                              1 << 24, None) == mis

@@ -10,6 +10,7 @@ using namespace moe::attn;
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 constexpr int kMaxTokens = 1 << 24;
 
@@ -44,7 +45,7 @@ int check_rope(const moe_attn_shape& a, const moe_rope& r, const int32_t* positi
     if (r.dims < 0 || r.dims % 2 != 0 || r.dims > a.D || r.positions < 1 || !r.table ||
         !positions || (r.layout != MOE_ROPE_HALF && r.layout != MOE_ROPE_INTERLEAVED))
         return MOE_ERR_INVALID_ARG;
-    if (!aligned16(r.table)) return MOE_ERR_MISALIGNED;
+    if (!aligned16(r.table) || !aligned4(positions)) return MOE_ERR_MISALIGNED;
     return MOE_OK;
 }
 
@@ -74,6 +75,7 @@ int check_packed(const moe_packed& s) {
         if (const int rc = check_tokens(T)) return rc;
     if (s.B > 65535) return MOE_ERR_UNSUPPORTED_SHAPE;
     if ((!s.cu_q || !s.cu_k) && s.B > 0) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(s.cu_q) || !aligned4(s.cu_k)) return MOE_ERR_MISALIGNED;
     return MOE_OK;
 }
 
@@ -194,9 +196,7 @@ int moe_norm_rope_backward(moe_attn_shape a, int32_t T, moe_heads dq_out, moe_he
         }
         if (wq) {
             if (!dwq || (!dwk && with_k) || !ws) return MOE_ERR_INVALID_ARG;
-            if (!aligned16(ws) || (reinterpret_cast<uintptr_t>(dwq) & 3u) ||
-                (reinterpret_cast<uintptr_t>(dwk) & 3u))
-                return MOE_ERR_MISALIGNED;
+            if (!aligned16(ws) || !aligned4(dwq) || !aligned4(dwk)) return MOE_ERR_MISALIGNED;
             if (ws_bytes < moe_norm_rope_workspace_size(a, T)) return MOE_ERR_WORKSPACE_TOO_SMALL;
         } else if (T == 0) {
             return MOE_OK;
@@ -348,6 +348,7 @@ int moe_attention_decode(moe_attn_shape a, int32_t B, int32_t n, int32_t max_kv,
         ATTN_TRY(check_heads(&q, T, a.Hq, a.D, false));
         ATTN_TRY(check_heads(&out, T, a.Hq, a.D, true));
         if (!block_table || !kv_lens) return MOE_ERR_INVALID_ARG;
+        if (!aligned4(block_table) || !aligned4(kv_lens)) return MOE_ERR_MISALIGNED;
         if (table_stride < 0 ||
             (static_cast<int64_t>(max_kv) + cache.page_size - 1) / cache.page_size > table_stride)
             return MOE_ERR_INVALID_ARG;
