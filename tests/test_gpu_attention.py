@@ -474,3 +474,65 @@ def test_decoder_block_example():
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
     assert m.main() < 1e-2
+
+
+@pytest.mark.parametrize("case", NR)
+def test_norm_rope_backward_in_place(case):
+    """dq and dk over the gradients they come from, in one fused array: the same bits,
+    and the values between them stay."""
+    T, Hq, Hkv, D, rot, layout, norm = case
+    att, qkv, (wq, wk), _, pos, _ = norm_rope_data(case, 3)
+    q, k = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv]
+    g = rnd(tuple(qkv.shape), 52).cuda()
+    kept = g.clone()
+    want = att.norm_rope_backward(kept[:, :Hq], kept[:, Hq:Hq + Hkv], q, k, wq, wk, pos)
+    got = att.norm_rope_backward(g[:, :Hq], g[:, Hq:Hq + Hkv], q, k, wq, wk, pos, dq=g[:, :Hq],
+                                 dk=g[:, Hq:Hq + Hkv])
+    for x, y in zip(want, got):
+        assert x is None or torch.equal(x, y)
+    assert torch.equal(g[:, Hq + Hkv:], kept[:, Hq + Hkv:])
+
+
+def test_served_tokens_from_a_graph():
+    """append and decode captured once and replayed with other lengths, pages and tokens:
+    the bits of the plain calls."""
+    from token_dispatch_grouped_gb300.attention import Attention
+    Hq, Hkv, D, page = 8, 2, 64, 16
+    att = Attention(Hq, Hkv, D, rope_table=table_of(256, D))
+    w = torch.ones(D, device="cuda")
+    kp = rnd((24, Hkv, page, D), 5).cuda()
+    vp = rnd((24, Hkv, page, D), 6).cuda()
+    table = torch.arange(24, dtype=torch.int32, device="cuda").view(3, 8)
+    qkv = torch.zeros(3, Hq + 2 * Hkv, D, dtype=torch.bfloat16, device="cuda")
+    kv = torch.ones(3, dtype=torch.int32, device="cuda")
+    pos = torch.zeros(3, dtype=torch.int32, device="cuda")
+    slots = torch.zeros(3, dtype=torch.int64, device="cuda")
+
+    def step(kp, vp):
+        q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+        return att.decode(att.append(q, k, v, w, w, pos, slots, kp, vp), kp, vp, table, kv, 128)
+
+    def fill(i):
+        lens = torch.tensor([1 + 40 * i, 17 + i, 128 - i], dtype=torch.int32)
+        qkv.copy_(rnd(tuple(qkv.shape), 70 + i))
+        kv.copy_(lens)
+        pos.copy_(lens - 1)
+        at = (lens - 1).long()
+        slots.copy_(table.cpu().long()[torch.arange(3), at // page] * page + at % page)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    fill(0)
+    with torch.cuda.stream(side):
+        step(kp.clone(), vp.clone())
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(kp, vp)
+    for i in (1, 2, 0):
+        fill(i)
+        ck, cv = kp.clone(), vp.clone()
+        graph.replay()
+        want = step(ck, cv)
+        assert torch.equal(out, want) and torch.equal(kp, ck) and torch.equal(vp, cv)
