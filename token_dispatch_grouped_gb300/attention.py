@@ -62,7 +62,9 @@ class Attention:
     eps: of the RMS norm of the heads. rope_table: from rope_table() (None: no
     rotation); rope_layout "half" or "interleaved". scale: of the scores, by
     default D^-1/2. Calls run on the current stream. The workspace is kept, grows to the
-    largest call and is shared by all of them: use one Attention per stream."""
+    largest call and is shared by all of them: use one Attention per stream. Workspaces that
+    were outgrown are kept too, as a captured CUDA graph goes on using the one that its calls
+    were given: a graph holds as long as its Attention does."""
 
     def __init__(self, Hq: int, Hkv: int, D: int, device="cuda", eps: float = 1e-6,
                  rope_table: torch.Tensor | None = None, rope_layout: str = "half",
@@ -81,7 +83,7 @@ class Attention:
                 raise B.MoeError(B.MOE_ERR_INVALID_ARG, "Attention: rope_table")
             self.rope = B.MoeRope(rope_table.data_ptr(), rope_table.shape[0],
                                   2 * rope_table.shape[1], B.ROPE_LAYOUTS[rope_layout])
-        self._ws = None
+        self._ws = []  # the last one is in use
 
     # ---------------------------------------------------------------- checks
     def _heads(self, t, T: int, H: int, where: str) -> B.MoeHeads:
@@ -110,9 +112,13 @@ class Attention:
     def _workspace(self, nbytes: int):
         if nbytes == 0:
             return None
-        if self._ws is None or self._ws.numel() < nbytes:
-            self._ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        return self._ws
+        if not self._ws or self._ws[-1].numel() < nbytes:
+            # at least twice the last one: those kept for graphs stay smaller together
+            # than the one in use
+            least = 2 * self._ws[-1].numel() if self._ws else 0
+            self._ws.append(torch.empty(max(nbytes, least), dtype=torch.uint8,
+                                        device=self.device))
+        return self._ws[-1]
 
     # ------------------------------------------------------- norm and positions
     def norm_rope(self, q, k, wq, wk, positions, q_out=None, k_out=None):
