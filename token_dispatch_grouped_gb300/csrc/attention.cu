@@ -348,8 +348,12 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
                 for (int e = 4; e < 124; e += 8)
 #pragma unroll
                     for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], s[e + 2 * u], s[e + 2 * u + 1]);
-                const float top = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], s[124], s[125]),
-                                       fmaxf(s[126], s[127]));
+                // (a row that sees no key may hold anything, and has no say in the vote below:
+                // m moves in all rows of the warp, and with it how their p is rounded)
+                const float top = mine <= 0 ? -INFINITY
+                                            : max3(max3(mx[0], mx[1], mx[2]),
+                                                   max3(mx[3], s[124], s[125]),
+                                                   fmaxf(s[126], s[127]));
                 if (j == 0) {
                     m = top;
                 } else if (__any_sync(~0u, (top - m) * c > 8.f)) {
