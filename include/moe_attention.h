@@ -24,8 +24,12 @@
  *   - What only the device can see (offsets that do not ascend or pass the
  *     arrays, a sequence longer than the stated bound, a position outside the
  *     rotary table, a slot or page outside the cache) sets MOE_ERR_BAD_INDEX in
- *     the status word; results of the row or sequence concerned are undefined.
- *     Nothing is read or written out of bounds.
+ *     the status word. Results of the row or sequence concerned are undefined (of
+ *     every sequence that shares rows with another, where offsets do not ascend);
+ *     a weight gradient is the sum without the row. All other results of the call
+ *     are what they are without it, and later calls of this header run too: only
+ *     after another error do they nothing. (The layer's calls do nothing after any,
+ *     see moe.h.) Nothing is read or written out of bounds.
  *   - Sums, softmax statistics and norms are fp32; results are rounded once to
  *     bf16. Where a product runs on the tensor cores, the softmax weights and
  *     their gradients are its bf16 operands. Every result is the same from run to

@@ -147,8 +147,9 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 10) {
             // ----------------------------------------- items, one ahead of the others
-            if ((sQ & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
-            const int skip = has_error(p.err);
+            const bool off = (sQ & 1023u) != 0;  // the swizzle's unit
+            if (off) raise_error(p.err, MOE_ERR_MISALIGNED);
+            const bool skip = __any_sync(~0u, off || stopped(p.err));
             for (int i = 0;; ++i) {
                 // snake order: forwards through the CTAs, then backwards
                 const int index = i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
@@ -435,7 +436,7 @@ attention_forward_kernel(const __grid_constant__ CUtensorMap mapQ,
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (threadIdx.x == 0 && *abort_flag) raise_error(p.err, MOE_ERR_TIMEOUT);
+    if (threadIdx.x == 0 && *abort_flag) raise_timeout(p.err);
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
 

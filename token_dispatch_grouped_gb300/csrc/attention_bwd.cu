@@ -161,8 +161,9 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
 
     if (warp == kCompute + 2) {
         // --------------------------------------------- items, one ahead of the others
-        if ((sQ & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
-        const int skip = has_error(p.err);
+        const bool off = (sQ & 1023u) != 0;  // the swizzle's unit
+        if (off) raise_error(p.err, MOE_ERR_MISALIGNED);
+        const bool skip = __any_sync(~0u, off || stopped(p.err));
         for (int i = 0;; ++i) {
             // snake order: forwards through the CTAs, then backwards
             const int index = i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
@@ -432,7 +433,7 @@ dq_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUte
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (threadIdx.x == 0 && *abort_flag) raise_error(p.err, MOE_ERR_TIMEOUT);
+    if (threadIdx.x == 0 && *abort_flag) raise_timeout(p.err);
     if (warp == kCompute) tmem_dealloc(tmem, 512);
 }
 
@@ -490,8 +491,9 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
     pdl_wait();
     pdl_trigger();
     if (warp == 0) {
-        if ((sK & 1023u) != 0) raise_error(p.err, MOE_ERR_MISALIGNED);  // the swizzle's unit
-        const bool skip = has_error(p.err);
+        const bool off = (sK & 1023u) != 0;  // the swizzle's unit
+        if (off) raise_error(p.err, MOE_ERR_MISALIGNED);
+        const bool skip = __any_sync(~0u, off || stopped(p.err));
         Work w = find_work<true>(p.s, tpt, blockIdx.x / p.a.Hkv, lane, p.err);
         if (skip) w.items = 0;
         if (lane == 0) *found = w;
@@ -678,7 +680,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUt
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (threadIdx.x == 0 && *abort_flag) raise_error(p.err, MOE_ERR_TIMEOUT);
+    if (threadIdx.x == 0 && *abort_flag) raise_timeout(p.err);
     if (warp == kCompute) tmem_dealloc(tmem, 512);
 }
 

@@ -26,6 +26,19 @@ struct Packed {
     const int32_t *cu_q, *cu_k;
 };
 
+// Whether the attention kernels stop. A bad index concerns its row or sequence alone, and
+// every kernel checks the indices that it uses, so the others go on with the rest of the call
+// and with later calls; any other error may have left anything behind it.
+__device__ __forceinline__ bool stopped(const int* err) {
+    const int code = *reinterpret_cast<const volatile int*>(err);
+    return code != MOE_OK && code != MOE_ERR_BAD_INDEX;
+}
+// A wait that ran out concerns the call, and is reported over a bad index.
+__device__ __forceinline__ void raise_timeout(int* err) {
+    if (atomicCAS(err, MOE_OK, MOE_ERR_TIMEOUT) == MOE_ERR_BAD_INDEX)
+        atomicCAS(err, MOE_ERR_BAD_INDEX, MOE_ERR_TIMEOUT);
+}
+
 // Sequence b's rows [q0, q0 + nq) and [k0, k0 + nk). False (and MOE_ERR_BAD_INDEX)
 // if its offsets do not ascend within the arrays or it is longer than stated.
 __device__ __forceinline__ bool sequence_of(const Packed& s, int b, int& q0, int& nq, int& k0,

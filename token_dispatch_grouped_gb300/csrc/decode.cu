@@ -113,7 +113,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
     const int G = p.a.Hq / p.a.Hkv, D = p.a.D;
     const int len = p.lens[b];
     const int t0 = part * p.chunk;
-    const bool skip = has_error(p.err);
+    const bool skip = stopped(p.err);
     // an empty sequence has one part, which writes its zeros
     if (__syncthreads_or(skip) || len < 0 || len > p.max_kv || (part > 0 && t0 >= len)) {
         if (threadIdx.x == 0 && (len < 0 || len > p.max_kv)) raise_error(p.err, MOE_ERR_BAD_INDEX);
@@ -339,7 +339,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
         }
     }
     __syncthreads();
-    if (threadIdx.x == 0 && *abort_flag) raise_error(p.err, MOE_ERR_TIMEOUT);
+    if (threadIdx.x == 0 && *abort_flag) raise_timeout(p.err);
 }
 
 // Joins the parts of each row, in part order: one warp a row, four columns a lane.
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(128) join_kernel(const Params p) {
     pdl_trigger();
     const int lane = threadIdx.x & 31;
     const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (__any_sync(~0u, has_error(p.err))) return;
+    if (__any_sync(~0u, stopped(p.err))) return;
     const int n = p.n, Hq = p.a.Hq, D = p.a.D;
     if (row >= static_cast<long long>(p.B) * n * Hq) return;
     const long long t = row / Hq;

@@ -187,7 +187,7 @@ norm_rope_kernel(const NormRope p, const Runs rn) {
     };
     // what does not depend on another load comes first, all of it in flight at once
     load(in_row, r0);
-    const bool skip = has_error(p.err);
+    const bool skip = stopped(p.err);
     int positions = 0;  // lane i: of token t0 + i
     if (SWAP != SWAP_NONE && kind < 2 && lane < NT && t0 + lane < p.T) positions = p.positions[t0 + lane];
     const long long slot = APPEND && kind > 0 ? p.slots[t0] : 0;
@@ -322,7 +322,7 @@ norm_rope_backward_kernel(const NormRope p, Heads dq_out, Heads dk_out, float* p
     __shared__ float s_dw[kWarps][2][128];
     pdl_wait();
     pdl_trigger();
-    if (has_error(p.err)) return;
+    if (stopped(p.err)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int piece = lane % LPR, sub = lane / LPR;
     const int D = p.a.D;
@@ -484,7 +484,7 @@ norm_rope_dw_kernel(const float* part, int parts, int D, float* dwq, float* dwk,
     __shared__ float s[32][33];
     pdl_wait();
     pdl_trigger();
-    if (has_error(err)) return;
+    if (stopped(err)) return;
     const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + cx;
     float v = 0.f;
@@ -506,7 +506,7 @@ __global__ void rope_table_kernel(long long n, int half, const double* inv_freq,
                                   float2* table, int* err) {
     pdl_wait();
     pdl_trigger();
-    if (has_error(err)) return;
+    if (stopped(err)) return;
     const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (i >= n) return;
     double s, c;
