@@ -138,9 +138,10 @@ int moe_attention_backward(moe_attn_shape a, moe_packed s, float scale, moe_head
 
 /* Attention of the newest n tokens of B sequences over the paged cache (their own
  * keys and values already in it). q, out: [B * n, Hq, D], rows b * n .. b * n + n
- * of sequence b; kv_lens [B] int32 counts its cached tokens, at most max_kv; token
- * t lies in row t % page_size of page block_table[b * table_stride + t /
- * page_size] (int32; entries past a sequence's pages are not read). Query i sees
+ * of sequence b; kv_lens [B] int32 counts its cached tokens, at most max_kv (no
+ * more than 2^30); token t lies in row t % page_size of page
+ * block_table[b * table_stride + t / page_size] (int32; entries past a sequence's
+ * pages are not read). Query i sees
  * the tokens j <= i + kv_lens[b] - n; one that sees none gets zeros. The keys are
  * split over CTAs where B, Hkv and n leave the GPU idle, and the parts joined in a
  * fixed order. */

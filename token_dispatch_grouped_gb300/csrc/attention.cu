@@ -445,7 +445,6 @@ cudaError_t forward(const Attention& p, cudaStream_t st) {
     using C = Cfg<DP>;
     const int G = p.a.Hq / p.a.Hkv, D = p.a.D, tpt = kRows / G;
     const long long items = tile_bound(p.s.Tq, p.s.B, p.s.max_q, 2 * tpt);
-    if (items == 0) return cudaSuccess;
     Params prm{p.a, p.s, p.scale, p.out, p.lse, p.err, tpt, static_cast<int>(items)};
     CUtensorMap mq, mk, mv;
     if (!make_tmap_heads(&mq, p.q, p.s.Tq, p.a.Hq, D, G, tpt)) return cudaErrorInvalidValue;

@@ -702,7 +702,7 @@ cudaError_t backward(const Attention& p, cudaStream_t st) {
     if (p.s.Tq == 0) mq = md = mk;
     if (p.s.Tk == 0) mk = mv = mq;
     const long long items = static_cast<long long>(prm.items) * p.a.Hkv;
-    if (p.s.Tq > 0 && items > 0) {
+    if (p.s.Tq > 0) {
         auto kfn = dq_kernel<DP>;
         cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              C::SMEM_Q);
@@ -712,8 +712,8 @@ cudaError_t backward(const Attention& p, cudaStream_t st) {
                      mq, md, mk, mv, prm);
         if (e != cudaSuccess) return e;
     }
+    if (p.s.Tk == 0) return cudaSuccess;
     const long long ki = tile_bound(p.s.Tk, p.s.B, p.s.max_k, kRows);
-    if (p.s.Tk == 0 || ki == 0) return cudaSuccess;
     auto kfn = dkv_kernel<DP>;
     const cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                C::SMEM_KV);

@@ -1,5 +1,6 @@
 // attn_api.cu — the C ABI of the attention operators (include/moe_attention.h):
 // argument checks, workspace sizes and launches.
+#include <algorithm>
 #include <cmath>
 
 #include "attn.cuh"
@@ -13,6 +14,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 constexpr int kMaxTokens = 1 << 24;
+constexpr int kMaxCached = 1 << 30;  // of a sequence: token arithmetic stays within 32 bits
 
 int check_attn(const moe_attn_shape& a) {
     if (a.Hq < 1 || a.Hkv < 1 || a.D < 1) return MOE_ERR_INVALID_ARG;
@@ -120,8 +122,10 @@ NormRope norm_rope_of(const moe_attn_shape& a, int32_t T, const moe_heads& q, co
     return p;
 }
 
+// No sequence is longer than its array, so a larger stated bound says no more than that.
 Packed packed_of(const moe_packed& s) {
-    return {s.B, s.Tq, s.Tk, s.max_q, s.max_k, s.causal, s.cu_q, s.cu_k};
+    return {s.B, s.Tq, s.Tk, std::min(s.max_q, s.Tq), std::min(s.max_k, s.Tk), s.causal, s.cu_q,
+            s.cu_k};
 }
 
 }  // namespace
@@ -326,7 +330,7 @@ int moe_attention_backward(moe_attn_shape a, moe_packed s, float scale, moe_head
 
 size_t moe_attention_decode_workspace_size(moe_attn_shape a, int32_t B, int32_t n,
                                            int32_t max_kv) {
-    if (check_attn(a) || B < 1 || n < 1 || max_kv < 1 ||
+    if (check_attn(a) || B < 1 || n < 1 || max_kv < 1 || max_kv > kMaxCached ||
         static_cast<int64_t>(B) * n > kMaxTokens)
         return 0;
     return sizeof(float) * decode_ws_floats(a, B, n, max_kv);
@@ -342,7 +346,8 @@ int moe_attention_decode(moe_attn_shape a, int32_t B, int32_t n, int32_t max_kv,
         ATTN_TRY(check_cache(a, cache, &shift));
         ATTN_TRY(check_scale(scale));
         if (B < 0 || n < 1 || max_kv < 0) return MOE_ERR_INVALID_ARG;
-        if (static_cast<int64_t>(B) * n > kMaxTokens) return MOE_ERR_UNSUPPORTED_SHAPE;
+        if (static_cast<int64_t>(B) * n > kMaxTokens || max_kv > kMaxCached)
+            return MOE_ERR_UNSUPPORTED_SHAPE;
         if (B == 0) return MOE_OK;
         const int32_t T = B * n;
         ATTN_TRY(check_heads(&q, T, a.Hq, a.D, false));

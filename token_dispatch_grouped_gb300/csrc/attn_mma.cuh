@@ -279,11 +279,12 @@ __device__ __forceinline__ Work find_work(const Packed& s, int tile, int want, i
     }
     return {0, 0, 0, 0, 0, 0};
 }
-// Upper bound of the items, known on the host.
+// Upper bound of the items, known on the host; `longest` <= T. At least one, so that some
+// CTA looks the sequences over.
 inline long long tile_bound(int T, int B, int longest, int tile) {
     const long long a = static_cast<long long>(T) / tile + B;
     const long long b = static_cast<long long>(B) * ((longest + tile - 1) / tile);
-    return a < b ? a : b;
+    return a < b ? a : b < 1 ? 1 : b;
 }
 
 // One warp looks all sequences over (for the error report).
