@@ -442,7 +442,8 @@ norm_rope_backward_kernel(const NormRope p, Heads dq_out, Heads dk_out, float* p
                         }
                         // rows past the run (zeros) and rows left out add nothing
                         float rr = rsqrtf(row_sum<LPR>(s0 + s1) * inv_d + p.eps);
-                        const float k = -rr * rr * rr * (row_sum<LPR>(q0 + q1) * inv_d);
+                        // (r^3 alone would leave fp32 where r is beyond 2^42 either way)
+                        const float k = -(rr * rr) * (rr * (row_sum<LPR>(q0 + q1) * inv_d));
                         if (mine) {
 #pragma unroll
                             for (int e = 0; e < 8; e += 2) {
