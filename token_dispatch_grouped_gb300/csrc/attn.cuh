@@ -26,6 +26,23 @@ struct Packed {
     const int32_t *cu_q, *cu_k;
 };
 
+// launch_k for kernels that are launched programmatically by default, as the grouped GEMMs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                       Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled(true) ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
 // Whether the attention kernels stop. A bad index concerns its row or sequence alone, and
 // every kernel checks the indices that it uses, so the others go on with the rest of the call
 // and with later calls; any other error may have left anything behind it.

@@ -3,7 +3,26 @@
 #include <algorithm>
 #include <cmath>
 
-#include "attn.cuh"
+#include "attn_mma.cuh"
+
+namespace moe {
+namespace attn {
+bool make_tmap_heads(CUtensorMap* map, const Heads& h, int T, int H, int D, uint32_t box_heads,
+                     uint32_t box_tokens) {
+    auto fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
+                          static_cast<cuuint64_t>(T)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(h.hs) * 2, static_cast<cuuint64_t>(h.ts) * 2};
+    cuuint32_t box[3] = {64, box_heads, box_tokens};
+    cuuint32_t es[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, h.p, dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace attn
+}  // namespace moe
 
 using namespace moe;
 using namespace moe::attn;

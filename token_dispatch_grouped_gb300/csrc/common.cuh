@@ -6,6 +6,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -42,9 +43,9 @@ inline bool pdl_enabled(bool gemm_launch = false) {
 // kernel<<<grid, block, smem, st>>>(args...), with programmatic stream
 // serialization where pdl_enabled() says so; the kernel calls pdl_wait() before
 // it touches global memory.
-template <bool GEMM_LAUNCH, typename... KArgs, typename... Args>
-cudaError_t launch_as(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                      Args&&... args) {
+template <typename... KArgs, typename... Args>
+cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                     Args&&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
@@ -54,19 +55,8 @@ cudaError_t launch_as(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sm
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl_enabled(GEMM_LAUNCH) ? 1 : 0;
+    cfg.numAttrs = pdl_enabled() ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
-}
-template <typename... KArgs, typename... Args>
-cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                     Args&&... args) {
-    return launch_as<false>(kernel, grid, block, smem, st, static_cast<KArgs>(args)...);
-}
-// The same for kernels that are launched programmatically by default, as the grouped GEMMs.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                       Args&&... args) {
-    return launch_as<true>(kernel, grid, block, smem, st, static_cast<KArgs>(args)...);
 }
 
 // Device status word layout: the first error code that was raised wins.
@@ -93,6 +83,9 @@ struct LaunchScope {
     cudaStream_t st_;
     int slot_;
 };
+
+// The driver's tensor map encoder; nullptr if it has none.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // Tensor map of a 2D row-major bf16 array [rows, cols] with a box of
 // box_cols x box_rows and a swizzle of `swizzle` bytes (128, 64, or 0 for
