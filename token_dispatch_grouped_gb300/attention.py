@@ -55,7 +55,7 @@ def rope_table(positions: int, inv_freq: torch.Tensor, scale: float = 1.0,
 
 class Attention:
     """The attention of a decoder block: Hq query heads on Hkv key/value heads of D
-    values, on a CUDA device. Tensors of heads are bf16 [tokens, heads, D] with
+    values, on the current CUDA device. Tensors of heads are bf16 [tokens, heads, D] with
     dense values; their token and head strides are free (multiples of 8), so views
     of a fused projection are taken as they are.
 
@@ -169,7 +169,7 @@ class Attention:
                 lse=None):
         """out [Tq, Hq, D] and lse [Tq, Hq] of the sequences between the offsets cu_q
         and cu_k (int32, on the device; cu_k = None: those of the queries). max_q and
-        max_k bound their lengths."""
+        max_k bound their lengths. Rows of no sequence are not written."""
         Tq, Tk, Hq, Hkv, where = q.shape[0], k.shape[0], self.Hq, self.Hkv, "attention_forward"
         if out is None:
             out = self._out(Tq, Hq)
@@ -185,7 +185,7 @@ class Attention:
 
     def backward(self, dout, q, k, v, out, lse, cu_q, max_q, cu_k=None, max_k=None, causal=True,
                  dq=None, dk=None, dv=None):
-        """dq, dk, dv of forward()."""
+        """dq, dk, dv of forward(), at the rows that belong to a sequence."""
         Tq, Tk, Hq, Hkv, where = q.shape[0], k.shape[0], self.Hq, self.Hkv, "attention_backward"
         if dq is None:
             dq = self._out(Tq, Hq)
@@ -258,6 +258,8 @@ class Attention:
         return out
 
     def check_error(self) -> None:
+        """Waits for the device and raises what it has reported since the last check. After a
+        bad index (MOE_ERR_BAD_INDEX) the other rows and sequences hold."""
         rc = B.moe_get_error()
         if rc != B.MOE_OK:
             raise B.MoeError(rc, "device")
