@@ -2,8 +2,9 @@
  * moe_attention.h — C ABI of the attention operators that stand beside the MoE
  * layer of a decoder block (NVIDIA GB300, sm_103a): norm and rotary positions of
  * the query and key heads, attention over packed sequences with its backward,
- * appending to a paged key/value cache, and attention of the newest tokens over
- * that cache.
+ * appending to a paged key/value cache, attention of the newest tokens over that
+ * cache, and a smaller cache: 8 bits a value, sums of the softmax weights of every
+ * cached token, and eviction of the tokens that have few.
  *
  * Conventions (pointers, streams, errors, ownership) are those of moe.h. Beside
  * them:
@@ -150,6 +151,97 @@ int moe_attention_decode(moe_attn_shape a, int32_t B, int32_t n, int32_t max_kv,
                          moe_heads q, moe_kv_cache cache, const int32_t* block_table,
                          int32_t table_stride, const int32_t* kv_lens, moe_heads out, void* ws,
                          size_t ws_bytes, void* stream);
+
+/* ---- A smaller cache -----------------------------------------------------
+ *
+ * Paged cache of 8 bits a value: k, v [pages][Hkv][page_size][D] e4m3 (float8_e4m3fn:
+ * largest value 448, no infinities), D a multiple of 16; the value that row i of a
+ * page's head stands for is its e4m3 value times k_scale[page][head] (v_scale). Pages
+ * as in moe_kv_cache. Scales are finite and not negative; those that
+ * moe_kv8_append writes are powers of two, so that a scale that grows moves the
+ * values already there without rounding them again (but for those that leave e4m3's
+ * normal range, which lose what their first rounding with that scale would have
+ * lost). */
+typedef struct {
+    void *k, *v;              /* e4m3 */
+    float *k_scale, *v_scale; /* fp32 [pages][Hkv], 4-byte aligned */
+    int32_t pages, page_size;
+} moe_kv8_cache;
+
+/* moe_norm_rope of T new tokens, whose keys and values go into the 8-bit cache behind
+ * the tokens that their sequences have there. Sequence b of B has the new rows
+ * cu_new[b] .. cu_new[b + 1] (int32 [B + 1], as cu_q of moe_packed); kv_lens[b] counts
+ * its cached tokens with the new ones, at most max_kv, and token t lies in row
+ * t % page_size of page block_table[b * table_stride + t / page_size], as
+ * moe_attention_decode reads them. Rows of no sequence are not stored. All T queries
+ * go to q_out.
+ *   For every page and head that gets rows, with o the first of them:
+ *   p = the smallest power of two (2^-100 at least, 2^120 at most) with
+ *       |x| <= 448 p for every finite new value x;
+ *   scale = o > 0 ? max(scale, p) : p       (what a page held before its row 0 is
+ *       written anew has no say);
+ *   if the scale grew, rows 0 .. o - 1 are stored in it; the new rows are
+ *   e4m3(x / scale), rounded once from fp32 (keys) or bf16 (values). A value that is
+ *   not finite is stored as NaN.
+ * Pages of two sequences, or twice in one, must not be the same where the call writes.
+ * Where cu_new does not ascend, nothing holds of what the call stores. */
+int moe_kv8_append(moe_attn_shape a, int32_t B, int32_t T, int32_t max_kv, moe_heads q,
+                   moe_heads k, moe_heads v, const float* wq, const float* wk, float eps,
+                   const int32_t* positions, moe_rope rope, const int32_t* cu_new,
+                   const int32_t* block_table, int32_t table_stride, const int32_t* kv_lens,
+                   moe_heads q_out, moe_kv8_cache cache, void* stream);
+
+/* moe_attention_decode that also adds up, for every cached token and key/value head,
+ * the softmax weights that the call gives it:
+ *   weights[page][head][row] = (t < kv_lens[b] - n and not fresh ? what it was : 0)
+ *                              + sum over the G query heads and the n queries
+ * (fp32 [pages][Hkv][page_size], 16-byte aligned). So a token's sum starts with the
+ * call in which it is among the newest, and `fresh` (0 or 1) starts those of all the
+ * sequences' tokens: after a prompt, a call with its last n tokens and `fresh` gives
+ * every token of it the weight that those n give. Rows past a sequence's length keep
+ * what they hold. Scores are kept in the workspace in fp32, 4 bytes for each of
+ * B * n * Hq rows and each of max_kv tokens (rounded up to 64). Two sequences must not
+ * share a page here: both would write its weights. */
+size_t moe_attention_decode_weights_workspace_size(moe_attn_shape a, int32_t B, int32_t n,
+                                                   int32_t max_kv);
+int moe_attention_decode_weights(moe_attn_shape a, int32_t B, int32_t n, int32_t max_kv,
+                                 float scale, moe_heads q, moe_kv_cache cache,
+                                 const int32_t* block_table, int32_t table_stride,
+                                 const int32_t* kv_lens, float* weights, int32_t fresh,
+                                 moe_heads out, void* ws, size_t ws_bytes, void* stream);
+
+/* moe_attention_decode over the 8-bit cache; weights (NULL: not kept) and fresh as
+ * moe_attention_decode_weights. with_weights: whether weights will be given. */
+size_t moe_attention_decode8_workspace_size(moe_attn_shape a, int32_t B, int32_t n,
+                                            int32_t max_kv, int32_t with_weights);
+int moe_attention_decode8(moe_attn_shape a, int32_t B, int32_t n, int32_t max_kv, float scale,
+                          moe_heads q, moe_kv8_cache cache, const int32_t* block_table,
+                          int32_t table_stride, const int32_t* kv_lens, float* weights,
+                          int32_t fresh, moe_heads out, void* ws, size_t ws_bytes, void* stream);
+
+/* Eviction: of every sequence of more than `keep` tokens, each key/value head for
+ * itself keeps the newest `recent` tokens and, of the others, the keep - recent with
+ * the largest weights (equal ones: the earlier first; NaN below every number). What is
+ * kept goes, in order and with its weights, into the pages
+ * new_table[b * new_stride + i / page_size], i < min(kv_lens[b], keep); sequences of at
+ * most `keep` tokens are copied whole. Positions are in the keys already, so a shorter
+ * sequence is decoded as any other: new_lens[b] = min(kv_lens[b], keep) (new_lens may be
+ * kv_lens itself). kept [B][Hkv][keep] int32 gets the kept tokens' places in the old
+ * sequence, ascending, -1 past new_lens[b].
+ * The pages of new_table are distinct from each other and from those of block_table,
+ * which are only read: they may be shared by sequences. 8-bit pages: a new page's scale
+ * is the largest scale of the pages that its rows come from, and values of pages with a
+ * smaller one are rounded to it (powers of two: as moe_kv8_append moves rows).
+ * 1 <= keep, 0 <= recent <= keep, max_kv <= 2^30. A sequence with a length outside
+ * 0 .. max_kv gets kept = -1 and no length. */
+int moe_kv_evict(moe_attn_shape a, int32_t B, int32_t max_kv, int32_t keep, int32_t recent,
+                 moe_kv_cache cache, float* weights, const int32_t* block_table,
+                 int32_t table_stride, const int32_t* kv_lens, const int32_t* new_table,
+                 int32_t new_stride, int32_t* new_lens, int32_t* kept, void* stream);
+int moe_kv8_evict(moe_attn_shape a, int32_t B, int32_t max_kv, int32_t keep, int32_t recent,
+                  moe_kv8_cache cache, float* weights, const int32_t* block_table,
+                  int32_t table_stride, const int32_t* kv_lens, const int32_t* new_table,
+                  int32_t new_stride, int32_t* new_lens, int32_t* kept, void* stream);
 
 #ifdef __cplusplus
 }

@@ -205,16 +205,39 @@ class Attention:
         return dq, dk, dv
 
     # --------------------------------------------------------------- paged cache
-    def _cache(self, k_pages, v_pages, where):
+    def _pages(self, k_pages, v_pages, where, dtype=torch.bfloat16):
         shape = k_pages.shape
         for x in (k_pages, v_pages):
-            if x.dtype is not torch.bfloat16 or x.dim() != 4 or x.shape != shape or \
+            if x.dtype is not dtype or x.dim() != 4 or x.shape != shape or \
                     not x.is_contiguous() or not x.is_cuda:
                 raise B.MoeError(B.MOE_ERR_INVALID_ARG, where)
         pages, heads, size, values = shape
         if heads != self.Hkv or values != self.D:
             raise B.MoeError(B.MOE_ERR_INVALID_ARG, where)
-        return B.MoeKvCache(k_pages.data_ptr(), v_pages.data_ptr(), pages, size)
+        return k_pages.data_ptr(), v_pages.data_ptr(), pages, size
+
+    def _cache(self, k_pages, v_pages, where):
+        return B.MoeKvCache(*self._pages(k_pages, v_pages, where))
+
+    def _cache8(self, k_pages, v_pages, k_scales, v_scales, where):
+        k, v, pages, size = self._pages(k_pages, v_pages, where, torch.float8_e4m3fn)
+        n = pages * self.Hkv
+        return B.MoeKv8Cache(k, v, self._ints(k_scales, n, where, torch.float32),
+                             self._ints(v_scales, n, where, torch.float32), pages, size)
+
+    def _weights(self, weights, cache, where):
+        return self._ints(weights, cache.pages * self.Hkv * cache.page_size, where, torch.float32)
+
+    def _table(self, table, nb, tokens, size, where):
+        """(pointer, stride) of a block table of nb sequences of at most `tokens` tokens."""
+        if table.dtype is not torch.int32 or table.dim() != 2 or not table.is_cuda:
+            raise B.MoeError(B.MOE_ERR_INVALID_ARG, where)
+        rows, wide = table.shape
+        stride = table.stride()
+        if rows != nb or (wide > 1 and stride[1] != 1) or (nb > 1 and stride[0] < wide) or \
+                tokens > wide * size:
+            raise B.MoeError(B.MOE_ERR_INVALID_ARG, where)
+        return table.data_ptr(), stride[0] if nb > 1 else wide
 
     def append(self, q, k, v, wq, wk, positions, slots, k_pages, v_pages, q_out=None):
         """norm_rope of new tokens; keys and values go to slots (int64) of the pages
@@ -231,31 +254,102 @@ class Attention:
                         self._cache(k_pages, v_pages, where))
         return q_out
 
-    def decode(self, q, k_pages, v_pages, block_table, kv_lens, max_kv, out=None):
+    def append8(self, q, k, v, wq, wk, positions, cu_new, block_table, kv_lens, k_pages, v_pages,
+                k_scales, v_scales, max_kv=None, q_out=None):
+        """append to a cache of 8 bits: pages float8_e4m3fn, one scale for each page and head
+        (k_scales, v_scales fp32 [pages, Hkv]). The new rows cu_new[b] .. cu_new[b + 1] of
+        sequence b go behind its tokens in the pages of block_table; kv_lens counts its tokens
+        with them, at most max_kv (None: as many as block_table has pages for)."""
+        T, nb, where = q.shape[0], kv_lens.numel(), "append8"
+        if q_out is None:
+            q_out = self._out(T, self.Hq)
+        cache = self._cache8(k_pages, v_pages, k_scales, v_scales, where)
+        if max_kv is None:
+            max_kv = min(block_table.shape[-1] * cache.page_size, 1 << 30)
+        table, stride = self._table(block_table, nb, max_kv, cache.page_size, where)
+        B.moe_kv8_append(self.a, nb, T, max_kv, self._heads(q, T, self.Hq, where),
+                         self._heads(k, T, self.Hkv, where), self._heads(v, T, self.Hkv, where),
+                         self._norm(wq, where), self._norm(wk, where), self.eps,
+                         self._positions(positions, T, where), self.rope,
+                         self._ints(cu_new, nb + 1, where), table, stride,
+                         self._ints(kv_lens, nb, where), self._heads(q_out, T, self.Hq, where),
+                         cache)
+        return q_out
+
+    def decode(self, q, k_pages, v_pages, block_table, kv_lens, max_kv, out=None, weights=None,
+               fresh=False):
         """Attention of the newest q.shape[0] / B tokens of B sequences, whose cached
         lengths (those tokens included) are kv_lens, at most max_kv. block_table
-        [B, pages of a sequence] int32."""
-        T, nb, where = q.shape[0], kv_lens.numel(), "decode"
+        [B, pages of a sequence] int32.
+
+        weights (fp32 [pages, Hkv, page_size]): the softmax weights that every cached token
+        gets in this call are added to it; those of the newest tokens, and with `fresh` of
+        all, start from zero."""
+        return self._decode(q, (k_pages, v_pages), block_table, kv_lens, max_kv, out, weights,
+                            fresh, "decode")
+
+    def decode8(self, q, k_pages, v_pages, k_scales, v_scales, block_table, kv_lens, max_kv,
+                out=None, weights=None, fresh=False):
+        """decode over the cache that append8 fills."""
+        return self._decode(q, (k_pages, v_pages, k_scales, v_scales), block_table, kv_lens,
+                            max_kv, out, weights, fresh, "decode8")
+
+    def _decode(self, q, pages, block_table, kv_lens, max_kv, out, weights, fresh, where):
+        T, nb, eight = q.shape[0], kv_lens.numel(), len(pages) == 4
         if out is None:
             out = self._out(T, self.Hq)
         if T == 0 and nb == 0:
             return out
-        if nb == 0 or T % nb or T < nb or block_table.dtype is not torch.int32 or \
-                block_table.dim() != 2 or not block_table.is_cuda:
+        if nb == 0 or T % nb or T < nb:
             raise B.MoeError(B.MOE_ERR_INVALID_ARG, where)
-        rows, wide = block_table.shape
-        stride = block_table.stride()
-        cache = self._cache(k_pages, v_pages, where)
-        if rows != nb or (wide > 1 and stride[1] != 1) or (nb > 1 and stride[0] < wide) or \
-                max_kv > wide * cache.page_size:
-            raise B.MoeError(B.MOE_ERR_INVALID_ARG, where)
+        cache = self._cache8(*pages, where) if eight else self._cache(*pages, where)
+        w = None if weights is None else self._weights(weights, cache, where)
+        table, stride = self._table(block_table, nb, max_kv, cache.page_size, where)
         n = T // nb
-        ws = self._workspace(B.moe_attention_decode_workspace_size(self.a, nb, n, max_kv))
-        B.moe_attention_decode(self.a, nb, n, max_kv, self.scale,
-                               self._heads(q, T, self.Hq, where), cache, block_table.data_ptr(),
-                               stride[0] if nb > 1 else wide, self._ints(kv_lens, nb, where),
-                               self._heads(out, T, self.Hq, where), ws)
+        args = (self.a, nb, n, max_kv, self.scale, self._heads(q, T, self.Hq, where), cache, table,
+                stride, self._ints(kv_lens, nb, where))
+        out_heads = self._heads(out, T, self.Hq, where)
+        if eight:
+            ws = self._workspace(B.moe_attention_decode8_workspace_size(self.a, nb, n, max_kv,
+                                                                        w is not None))
+            B.moe_attention_decode8(*args, w, bool(fresh), out_heads, ws)
+        elif w is None:
+            ws = self._workspace(B.moe_attention_decode_workspace_size(self.a, nb, n, max_kv))
+            B.moe_attention_decode(*args, out_heads, ws)
+        else:
+            ws = self._workspace(B.moe_attention_decode_weights_workspace_size(self.a, nb, n,
+                                                                               max_kv))
+            B.moe_attention_decode_weights(*args, w, bool(fresh), out_heads, ws)
         return out
+
+    def evict(self, k_pages, v_pages, weights, block_table, kv_lens, max_kv, keep, recent,
+              new_table, k_scales=None, v_scales=None, kept=None, new_lens=None):
+        """Cuts every sequence to `keep` tokens: for each key/value head the newest `recent`
+        and, of the others, those with the largest weights (as decode adds them up). They go
+        in order, with their weights, into the pages of new_table, which are none of those of
+        block_table; shorter sequences are copied. With k_scales and v_scales the pages are
+        those of append8. Returns new_lens [B] (may be kv_lens itself) and kept [B, Hkv, keep]
+        int32: the places in the old sequence, ascending, -1 past new_lens."""
+        nb, where = kv_lens.numel(), "evict"
+        if k_scales is None and v_scales is None:
+            cache, call = self._cache(k_pages, v_pages, where), B.moe_kv_evict
+        elif k_scales is None or v_scales is None:
+            raise B.MoeError(B.MOE_ERR_INVALID_ARG, where)
+        else:
+            cache = self._cache8(k_pages, v_pages, k_scales, v_scales, where)
+            call = B.moe_kv8_evict
+        if keep < 1 or recent < 0 or recent > keep:
+            raise B.MoeError(B.MOE_ERR_INVALID_ARG, where)
+        if kept is None:
+            kept = torch.empty(nb, self.Hkv, keep, dtype=torch.int32, device=self.device)
+        if new_lens is None:
+            new_lens = torch.empty(nb, dtype=torch.int32, device=self.device)
+        table, stride = self._table(block_table, nb, max_kv, cache.page_size, where)
+        goal, new_stride = self._table(new_table, nb, min(max_kv, keep), cache.page_size, where)
+        call(self.a, nb, max_kv, keep, recent, cache, self._weights(weights, cache, where), table,
+             stride, self._ints(kv_lens, nb, where), goal, new_stride,
+             self._ints(new_lens, nb, where), self._ints(kept, nb * self.Hkv * keep, where))
+        return new_lens, kept
 
     def check_error(self) -> None:
         """Waits for the device and raises what it has reported since the last check. After a

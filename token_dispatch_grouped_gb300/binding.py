@@ -69,6 +69,12 @@ class MoeKvCache(ctypes.Structure):
                 ("page_size", ctypes.c_int32)]
 
 
+class MoeKv8Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
+
+
 class MoePacked(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("Tq", ctypes.c_int32), ("Tk", ctypes.c_int32),
                 ("max_q", ctypes.c_int32), ("max_k", ctypes.c_int32), ("causal", ctypes.c_int32),
@@ -124,6 +130,23 @@ def _load() -> ctypes.CDLL:
         "moe_attention_decode": (I, [MoeAttnShape] + [ctypes.c_int32] * 3 +
                                  [ctypes.c_float, MoeHeads, MoeKvCache, P, ctypes.c_int32, P,
                                   MoeHeads, P, S, P]),
+        "moe_attention_decode_weights_workspace_size": (S, [MoeAttnShape] +
+                                                        [ctypes.c_int32] * 3),
+        "moe_attention_decode_weights": (I, [MoeAttnShape] + [ctypes.c_int32] * 3 +
+                                         [ctypes.c_float, MoeHeads, MoeKvCache, P,
+                                          ctypes.c_int32, P, P, ctypes.c_int32, MoeHeads, P, S,
+                                          P]),
+        "moe_attention_decode8_workspace_size": (S, [MoeAttnShape] + [ctypes.c_int32] * 4),
+        "moe_attention_decode8": (I, [MoeAttnShape] + [ctypes.c_int32] * 3 +
+                                  [ctypes.c_float, MoeHeads, MoeKv8Cache, P, ctypes.c_int32, P,
+                                   P, ctypes.c_int32, MoeHeads, P, S, P]),
+        "moe_kv8_append": (I, [MoeAttnShape] + [ctypes.c_int32] * 3 + [MoeHeads] * 3 +
+                           [P, P, ctypes.c_float, P, MoeRope, P, P, ctypes.c_int32, P, MoeHeads,
+                            MoeKv8Cache, P]),
+        "moe_kv_evict": (I, [MoeAttnShape] + [ctypes.c_int32] * 4 +
+                         [MoeKvCache, P, P, ctypes.c_int32, P, P, ctypes.c_int32, P, P, P]),
+        "moe_kv8_evict": (I, [MoeAttnShape] + [ctypes.c_int32] * 4 +
+                          [MoeKv8Cache, P, P, ctypes.c_int32, P, P, ctypes.c_int32, P, P, P]),
         "moe_get_error": (I, [P]),
         "moe_selftest_bounded_wait": (I, [ctypes.c_uint64, P]),
         "moe_status_string": (ctypes.c_char_p, [I]),
@@ -407,4 +430,65 @@ def moe_attention_decode(a, batch, n, max_kv, scale, q, cache, block_table, tabl
                                   _stream(stream))
     if check:
         _check(rc, "moe_attention_decode")
+    return rc
+
+
+# ------------------------------------------------ a smaller cache (moe_attention.h)
+def moe_kv8_append(a, batch, T, max_kv, q, k, v, wq, wk, eps, positions, rope, cu_new,
+                   block_table, table_stride, kv_lens, q_out, cache, stream=None, check=True):
+    rc = LIB.moe_kv8_append(a, batch, T, max_kv, heads(q), heads(k), heads(v), _ptr(wq),
+                            _ptr(wk), eps, _ptr(positions), rope, _ptr(cu_new),
+                            _ptr(block_table), table_stride, _ptr(kv_lens), heads(q_out), cache,
+                            _stream(stream))
+    if check:
+        _check(rc, "moe_kv8_append")
+    return rc
+
+
+def moe_attention_decode_weights_workspace_size(a, batch, n, max_kv) -> int:
+    return int(LIB.moe_attention_decode_weights_workspace_size(a, batch, n, max_kv))
+
+
+def moe_attention_decode_weights(a, batch, n, max_kv, scale, q, cache, block_table, table_stride,
+                                 kv_lens, weights, fresh, out, ws, stream=None, check=True):
+    rc = LIB.moe_attention_decode_weights(a, batch, n, max_kv, scale, heads(q), cache,
+                                          _ptr(block_table), table_stride, _ptr(kv_lens),
+                                          _ptr(weights), fresh, heads(out), _ptr(ws),
+                                          _nbytes(ws), _stream(stream))
+    if check:
+        _check(rc, "moe_attention_decode_weights")
+    return rc
+
+
+def moe_attention_decode8_workspace_size(a, batch, n, max_kv, with_weights) -> int:
+    return int(LIB.moe_attention_decode8_workspace_size(a, batch, n, max_kv, with_weights))
+
+
+def moe_attention_decode8(a, batch, n, max_kv, scale, q, cache, block_table, table_stride,
+                          kv_lens, weights, fresh, out, ws, stream=None, check=True):
+    rc = LIB.moe_attention_decode8(a, batch, n, max_kv, scale, heads(q), cache,
+                                   _ptr(block_table), table_stride, _ptr(kv_lens), _ptr(weights),
+                                   fresh, heads(out), _ptr(ws), _nbytes(ws), _stream(stream))
+    if check:
+        _check(rc, "moe_attention_decode8")
+    return rc
+
+
+def moe_kv_evict(a, batch, max_kv, keep, recent, cache, weights, block_table, table_stride,
+                 kv_lens, new_table, new_stride, new_lens, kept, stream=None, check=True):
+    rc = LIB.moe_kv_evict(a, batch, max_kv, keep, recent, cache, _ptr(weights),
+                          _ptr(block_table), table_stride, _ptr(kv_lens), _ptr(new_table),
+                          new_stride, _ptr(new_lens), _ptr(kept), _stream(stream))
+    if check:
+        _check(rc, "moe_kv_evict")
+    return rc
+
+
+def moe_kv8_evict(a, batch, max_kv, keep, recent, cache, weights, block_table, table_stride,
+                  kv_lens, new_table, new_stride, new_lens, kept, stream=None, check=True):
+    rc = LIB.moe_kv8_evict(a, batch, max_kv, keep, recent, cache, _ptr(weights),
+                           _ptr(block_table), table_stride, _ptr(kv_lens), _ptr(new_table),
+                           new_stride, _ptr(new_lens), _ptr(kept), _stream(stream))
+    if check:
+        _check(rc, "moe_kv8_evict")
     return rc

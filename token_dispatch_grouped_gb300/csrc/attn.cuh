@@ -2,6 +2,8 @@
 // head views, device helpers and the kernel launchers' signatures.
 #pragma once
 #include "../../include/moe_attention.h"
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 
 namespace moe {
@@ -159,16 +161,75 @@ struct Decode {
     int B, n, max_kv;
     float scale;
     Heads q, out;
-    const bf16 *k_pages, *v_pages;
+    const void *k_pages, *v_pages;      // bf16, or e4m3 with scales
+    const float *k_scale, *v_scale;     // nullptr: bf16
     int pages, page_shift;
     const int32_t* block_table;
     int table_stride;
     const int32_t* kv_lens;
-    float* part;
+    float* weights;                     // nullptr: not kept
+    int fresh;
+    float* ws;
     int* err;
 };
-size_t decode_ws_floats(const moe_attn_shape& a, int B, int n, int max_kv);
+size_t decode_ws_floats(const moe_attn_shape& a, int B, int n, int max_kv, bool weights);
 cudaError_t launch_attention_decode(const Decode& p, cudaStream_t st);
+
+// ---------------------------------------------------------------- cache8.cu
+// p: the keys (and values) of a NormRope without q, slots and pages.
+struct Append8 {
+    NormRope r;
+    int B, max_kv;
+    const int32_t *cu, *lens, *block_table;
+    int table_stride;
+    uint8_t *k_pages, *v_pages;
+    float *k_scale, *v_scale;
+};
+cudaError_t launch_append8(const Append8& p, cudaStream_t st);
+
+// ---------------------------------------------------------------- evict.cu
+struct Evict {
+    int Hkv, D, B, max_kv, keep, recent;
+    uint8_t *k_pages, *v_pages;    // rows of D values of 1 or 2 bytes
+    float *k_scale, *v_scale;      // nullptr: bf16
+    float* weights;
+    int pages, page_shift;
+    const int32_t *block_table, *lens, *new_table;
+    int table_stride, new_stride;
+    int32_t *new_lens, *kept;
+    int* err;
+};
+cudaError_t launch_evict(const Evict& p, cudaStream_t st);
+
+// ---------------------------------------------------------------- e4m3
+// Two values rounded to e4m3 (the first in the low byte), NaN where they are not finite.
+__device__ __forceinline__ float finite_or_nan(float x) {
+    return fabsf(x) <= 3.402823466e+38f ? x : __int_as_float(0x7fffffff);
+}
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(r)
+        : "f"(finite_or_nan(hi)), "f"(finite_or_nan(lo)));
+    return r;
+}
+// The two values of e4m3 pairs in fp16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(pair)));
+    return r;
+}
+// Four e4m3 values times f, rounded to e4m3 again.
+__device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t v, float f) {
+    uint32_t out = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t h = e4m3x2_to_f16x2(v >> (16 * i));
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        out |= to_e4m3x2(x.x * f, x.y * f) << (16 * i);
+    }
+    return out;
+}
 
 }  // namespace attn
 }  // namespace moe

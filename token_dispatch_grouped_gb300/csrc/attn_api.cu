@@ -32,6 +32,11 @@ namespace {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+#define ATTN_TRY(expr)               \
+    do {                             \
+        if (const int _rc = (expr)) return _rc; \
+    } while (0)
+
 constexpr int kMaxTokens = 1 << 24;
 constexpr int kMaxCached = 1 << 30;  // of a sequence: token arithmetic stays within 32 bits
 
@@ -89,6 +94,21 @@ int check_cache(const moe_attn_shape& a, const moe_kv_cache& c, int* shift) {
     return MOE_OK;
 }
 
+int check_cache8(const moe_attn_shape& a, const moe_kv8_cache& c, int* shift) {
+    ATTN_TRY(check_cache(a, moe_kv_cache{c.k, c.v, c.pages, c.page_size}, shift));
+    if (!c.k_scale || !c.v_scale) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(c.k_scale) || !aligned4(c.v_scale)) return MOE_ERR_MISALIGNED;
+    return a.D % 16 != 0 ? MOE_ERR_UNSUPPORTED_SHAPE : MOE_OK;
+}
+
+// A block table with `tokens` tokens' pages in every row, and the lengths beside it.
+int check_table(const int32_t* table, int32_t stride, const int32_t* lens, int64_t tokens,
+                int32_t page_size) {
+    if (!table || !lens) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(table) || !aligned4(lens)) return MOE_ERR_MISALIGNED;
+    return stride < 0 || (tokens + page_size - 1) / page_size > stride ? MOE_ERR_INVALID_ARG : MOE_OK;
+}
+
 int check_packed(const moe_packed& s) {
     if (s.B < 0 || s.max_q < 0 || s.max_k < 0 || (s.causal != 0 && s.causal != 1))
         return MOE_ERR_INVALID_ARG;
@@ -103,11 +123,6 @@ int check_packed(const moe_packed& s) {
 int check_scale(float scale) {
     return scale > 0.f && std::isfinite(scale) ? MOE_OK : MOE_ERR_INVALID_ARG;
 }
-
-#define ATTN_TRY(expr)               \
-    do {                             \
-        if (const int _rc = (expr)) return _rc; \
-    } while (0)
 
 int launched(cudaError_t e) { return e == cudaSuccess ? MOE_OK : cuda_error_status(e); }
 
@@ -139,6 +154,108 @@ NormRope norm_rope_of(const moe_attn_shape& a, int32_t T, const moe_heads& q, co
     p.interleaved = r.layout == MOE_ROPE_INTERLEAVED;
     p.err = err;
     return p;
+}
+
+// The attention of new tokens over a cache of either kind.
+struct Pages {
+    const void *k, *v;
+    const float *k_scale, *v_scale;  // nullptr: bf16
+    int pages, page_size, shift;
+};
+
+size_t decode_ws_bytes(const moe_attn_shape& a, int32_t B, int32_t n, int32_t max_kv, bool weights) {
+    if (check_attn(a) || B < 1 || n < 1 || max_kv < 1 || max_kv > kMaxCached ||
+        static_cast<int64_t>(B) * n > kMaxTokens)
+        return 0;
+    return sizeof(float) * decode_ws_floats(a, B, n, max_kv, weights);
+}
+
+int decode_of(const moe_attn_shape& a, int32_t B, int32_t n, int32_t max_kv, float scale, moe_heads q,
+              const Pages& c, const int32_t* block_table, int32_t table_stride, const int32_t* kv_lens,
+              float* weights, int32_t fresh, moe_heads out, void* ws, size_t ws_bytes, void* stream) {
+    ATTN_TRY(check_scale(scale));
+    if (B < 0 || n < 1 || max_kv < 0 || (fresh != 0 && fresh != 1)) return MOE_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(B) * n > kMaxTokens || max_kv > kMaxCached) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(weights)) return MOE_ERR_MISALIGNED;
+    if (B == 0) return MOE_OK;
+    const int32_t T = B * n;
+    ATTN_TRY(check_heads(&q, T, a.Hq, a.D, false));
+    ATTN_TRY(check_heads(&out, T, a.Hq, a.D, true));
+    ATTN_TRY(check_table(block_table, table_stride, kv_lens, max_kv, c.page_size));
+    const size_t need = decode_ws_bytes(a, B, n, max_kv, weights != nullptr);
+    if (need > 0 && !ws) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(ws)) return MOE_ERR_MISALIGNED;
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    int* err = device_status_word();
+    if (!err) return MOE_ERR_NO_DEVICE;
+    Decode p{};
+    p.a = a;
+    p.B = B;
+    p.n = n;
+    p.max_kv = max_kv;
+    p.scale = scale;
+    p.q = heads(q);
+    p.out = heads(out);
+    p.k_pages = c.k;
+    p.v_pages = c.v;
+    p.k_scale = c.k_scale;
+    p.v_scale = c.v_scale;
+    p.pages = c.pages;
+    p.page_shift = c.shift;
+    p.block_table = block_table;
+    p.table_stride = table_stride;
+    p.kv_lens = kv_lens;
+    p.weights = weights;
+    p.fresh = fresh;
+    p.ws = static_cast<float*>(ws);
+    p.err = err;
+    return launched(launch_attention_decode(p, static_cast<cudaStream_t>(stream)));
+}
+
+int evict_of(const moe_attn_shape& a, int32_t B, int32_t max_kv, int32_t keep, int32_t recent,
+             const Pages& c, float* weights, const int32_t* block_table, int32_t table_stride,
+             const int32_t* kv_lens, const int32_t* new_table, int32_t new_stride, int32_t* new_lens,
+             int32_t* kept, void* stream) {
+    if (B < 0 || max_kv < 0 || keep < 1 || recent < 0 || recent > keep) return MOE_ERR_INVALID_ARG;
+    if (B > kMaxTokens || max_kv > kMaxCached || static_cast<int64_t>(B) * a.Hkv >= (int64_t{1} << 31))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (B == 0) return MOE_OK;
+    if (!weights || !new_lens || !kept) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(weights) || !aligned4(new_lens) || !aligned4(kept)) return MOE_ERR_MISALIGNED;
+    ATTN_TRY(check_table(block_table, table_stride, kv_lens, max_kv, c.page_size));
+    ATTN_TRY(check_table(new_table, new_stride, kv_lens, std::min(max_kv, keep), c.page_size));
+    int* err = device_status_word();
+    if (!err) return MOE_ERR_NO_DEVICE;
+    Evict p{};
+    p.Hkv = a.Hkv;
+    p.D = a.D;
+    p.B = B;
+    p.max_kv = max_kv;
+    p.keep = keep;
+    p.recent = recent;
+    p.k_pages = static_cast<uint8_t*>(const_cast<void*>(c.k));
+    p.v_pages = static_cast<uint8_t*>(const_cast<void*>(c.v));
+    p.k_scale = const_cast<float*>(c.k_scale);
+    p.v_scale = const_cast<float*>(c.v_scale);
+    p.weights = weights;
+    p.pages = c.pages;
+    p.page_shift = c.shift;
+    p.block_table = block_table;
+    p.lens = kv_lens;
+    p.new_table = new_table;
+    p.table_stride = table_stride;
+    p.new_stride = new_stride;
+    p.new_lens = new_lens;
+    p.kept = kept;
+    p.err = err;
+    return launched(launch_evict(p, static_cast<cudaStream_t>(stream)));
+}
+
+Pages pages_of(const moe_kv_cache& c, int shift) {
+    return {c.k, c.v, nullptr, nullptr, c.pages, c.page_size, shift};
+}
+Pages pages_of(const moe_kv8_cache& c, int shift) {
+    return {c.k, c.v, c.k_scale, c.v_scale, c.pages, c.page_size, shift};
 }
 
 // No sequence is longer than its array, so a larger stated bound says no more than that.
@@ -349,10 +466,7 @@ int moe_attention_backward(moe_attn_shape a, moe_packed s, float scale, moe_head
 
 size_t moe_attention_decode_workspace_size(moe_attn_shape a, int32_t B, int32_t n,
                                            int32_t max_kv) {
-    if (check_attn(a) || B < 1 || n < 1 || max_kv < 1 || max_kv > kMaxCached ||
-        static_cast<int64_t>(B) * n > kMaxTokens)
-        return 0;
-    return sizeof(float) * decode_ws_floats(a, B, n, max_kv);
+    return decode_ws_bytes(a, B, n, max_kv, false);
 }
 
 int moe_attention_decode(moe_attn_shape a, int32_t B, int32_t n, int32_t max_kv, float scale,
@@ -363,43 +477,122 @@ int moe_attention_decode(moe_attn_shape a, int32_t B, int32_t n, int32_t max_kv,
         ATTN_TRY(check_attn(a));
         int shift = 0;
         ATTN_TRY(check_cache(a, cache, &shift));
-        ATTN_TRY(check_scale(scale));
-        if (B < 0 || n < 1 || max_kv < 0) return MOE_ERR_INVALID_ARG;
-        if (static_cast<int64_t>(B) * n > kMaxTokens || max_kv > kMaxCached)
-            return MOE_ERR_UNSUPPORTED_SHAPE;
-        if (B == 0) return MOE_OK;
-        const int32_t T = B * n;
+        return decode_of(a, B, n, max_kv, scale, q, pages_of(cache, shift), block_table, table_stride,
+                         kv_lens, nullptr, 0, out, ws, ws_bytes, stream);
+    });
+}
+
+size_t moe_attention_decode_weights_workspace_size(moe_attn_shape a, int32_t B, int32_t n,
+                                                   int32_t max_kv) {
+    return decode_ws_bytes(a, B, n, max_kv, true);
+}
+
+int moe_attention_decode_weights(moe_attn_shape a, int32_t B, int32_t n, int32_t max_kv,
+                                 float scale, moe_heads q, moe_kv_cache cache,
+                                 const int32_t* block_table, int32_t table_stride,
+                                 const int32_t* kv_lens, float* weights, int32_t fresh,
+                                 moe_heads out, void* ws, size_t ws_bytes, void* stream) {
+    return guarded([&]() -> int {
+        ATTN_TRY(check_attn(a));
+        int shift = 0;
+        ATTN_TRY(check_cache(a, cache, &shift));
+        if (!weights && B != 0) return MOE_ERR_INVALID_ARG;
+        return decode_of(a, B, n, max_kv, scale, q, pages_of(cache, shift), block_table, table_stride,
+                         kv_lens, weights, fresh, out, ws, ws_bytes, stream);
+    });
+}
+
+size_t moe_attention_decode8_workspace_size(moe_attn_shape a, int32_t B, int32_t n,
+                                            int32_t max_kv, int32_t with_weights) {
+    return a.D % 16 != 0 ? 0 : decode_ws_bytes(a, B, n, max_kv, with_weights != 0);
+}
+
+int moe_attention_decode8(moe_attn_shape a, int32_t B, int32_t n, int32_t max_kv, float scale,
+                          moe_heads q, moe_kv8_cache cache, const int32_t* block_table,
+                          int32_t table_stride, const int32_t* kv_lens, float* weights,
+                          int32_t fresh, moe_heads out, void* ws, size_t ws_bytes, void* stream) {
+    return guarded([&]() -> int {
+        ATTN_TRY(check_attn(a));
+        int shift = 0;
+        ATTN_TRY(check_cache8(a, cache, &shift));
+        return decode_of(a, B, n, max_kv, scale, q, pages_of(cache, shift), block_table, table_stride,
+                         kv_lens, weights, fresh, out, ws, ws_bytes, stream);
+    });
+}
+
+int moe_kv8_append(moe_attn_shape a, int32_t B, int32_t T, int32_t max_kv, moe_heads q,
+                   moe_heads k, moe_heads v, const float* wq, const float* wk, float eps,
+                   const int32_t* positions, moe_rope rope, const int32_t* cu_new,
+                   const int32_t* block_table, int32_t table_stride, const int32_t* kv_lens,
+                   moe_heads q_out, moe_kv8_cache cache, void* stream) {
+    return guarded([&]() -> int {
+        ATTN_TRY(check_attn(a));
+        ATTN_TRY(check_tokens(T));
+        int shift = 0;
+        ATTN_TRY(check_cache8(a, cache, &shift));
+        if (B < 0 || max_kv < 0) return MOE_ERR_INVALID_ARG;
+        if (B > 65535 || max_kv > kMaxCached) return MOE_ERR_UNSUPPORTED_SHAPE;
+        if (T == 0) return MOE_OK;
+        ATTN_TRY(check_rope(a, rope, positions));
+        ATTN_TRY(check_norm(wq, wk, eps));
         ATTN_TRY(check_heads(&q, T, a.Hq, a.D, false));
-        ATTN_TRY(check_heads(&out, T, a.Hq, a.D, true));
-        if (!block_table || !kv_lens) return MOE_ERR_INVALID_ARG;
-        if (!aligned4(block_table) || !aligned4(kv_lens)) return MOE_ERR_MISALIGNED;
-        if (table_stride < 0 ||
-            (static_cast<int64_t>(max_kv) + cache.page_size - 1) / cache.page_size > table_stride)
-            return MOE_ERR_INVALID_ARG;
-        const size_t need = moe_attention_decode_workspace_size(a, B, n, max_kv);
-        if (need > 0 && !ws) return MOE_ERR_INVALID_ARG;
-        if (!aligned16(ws)) return MOE_ERR_MISALIGNED;
-        if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+        ATTN_TRY(check_heads(&k, T, a.Hkv, a.D, false));
+        ATTN_TRY(check_heads(&v, T, a.Hkv, a.D, false));
+        ATTN_TRY(check_heads(&q_out, T, a.Hq, a.D, true));
+        if (B > 0) {
+            if (!cu_new) return MOE_ERR_INVALID_ARG;
+            if (!aligned4(cu_new)) return MOE_ERR_MISALIGNED;
+            ATTN_TRY(check_table(block_table, table_stride, kv_lens, max_kv, cache.page_size));
+        }
         int* err = device_status_word();
         if (!err) return MOE_ERR_NO_DEVICE;
-        Decode p{};
-        p.a = a;
+        Append8 p{};
+        p.r = norm_rope_of(a, T, q, k, wq, wk, eps, positions, rope, err);
+        p.r.v = heads(v);
+        p.r.q_out = heads(q_out);
+        p.r.pages = cache.pages;
+        p.r.page_shift = shift;
         p.B = B;
-        p.n = n;
         p.max_kv = max_kv;
-        p.scale = scale;
-        p.q = heads(q);
-        p.out = heads(out);
-        p.k_pages = static_cast<const bf16*>(cache.k);
-        p.v_pages = static_cast<const bf16*>(cache.v);
-        p.pages = cache.pages;
-        p.page_shift = shift;
+        p.cu = cu_new;
+        p.lens = kv_lens;
         p.block_table = block_table;
         p.table_stride = table_stride;
-        p.kv_lens = kv_lens;
-        p.part = static_cast<float*>(ws);
-        p.err = err;
-        return launched(launch_attention_decode(p, static_cast<cudaStream_t>(stream)));
+        p.k_pages = static_cast<uint8_t*>(cache.k);
+        p.v_pages = static_cast<uint8_t*>(cache.v);
+        p.k_scale = cache.k_scale;
+        p.v_scale = cache.v_scale;
+        const cudaStream_t st = static_cast<cudaStream_t>(stream);
+        if (B > 0) ATTN_TRY(launched(launch_append8(p, st)));
+        NormRope only_q = p.r;
+        only_q.k.p = nullptr;
+        return launched(launch_norm_rope(only_q, false, st));
+    });
+}
+
+int moe_kv_evict(moe_attn_shape a, int32_t B, int32_t max_kv, int32_t keep, int32_t recent,
+                 moe_kv_cache cache, float* weights, const int32_t* block_table,
+                 int32_t table_stride, const int32_t* kv_lens, const int32_t* new_table,
+                 int32_t new_stride, int32_t* new_lens, int32_t* kept, void* stream) {
+    return guarded([&]() -> int {
+        ATTN_TRY(check_attn(a));
+        int shift = 0;
+        ATTN_TRY(check_cache(a, cache, &shift));
+        return evict_of(a, B, max_kv, keep, recent, pages_of(cache, shift), weights, block_table,
+                        table_stride, kv_lens, new_table, new_stride, new_lens, kept, stream);
+    });
+}
+
+int moe_kv8_evict(moe_attn_shape a, int32_t B, int32_t max_kv, int32_t keep, int32_t recent,
+                  moe_kv8_cache cache, float* weights, const int32_t* block_table,
+                  int32_t table_stride, const int32_t* kv_lens, const int32_t* new_table,
+                  int32_t new_stride, int32_t* new_lens, int32_t* kept, void* stream) {
+    return guarded([&]() -> int {
+        ATTN_TRY(check_attn(a));
+        int shift = 0;
+        ATTN_TRY(check_cache8(a, cache, &shift));
+        return evict_of(a, B, max_kv, keep, recent, pages_of(cache, shift), weights, block_table,
+                        table_stride, kv_lens, new_table, new_stride, new_lens, kept, stream);
     });
 }
 
