@@ -200,7 +200,7 @@ int moe_kv8_append(moe_attn_shape a, int32_t B, int32_t T, int32_t max_kv, moe_h
  * sequences' tokens: after a prompt, a call with its last n tokens and `fresh` gives
  * every token of it the weight that those n give. Rows past a sequence's length keep
  * what they hold. Scores are kept in the workspace in fp32, 4 bytes for each of
- * B * n * Hq rows and each of max_kv tokens (rounded up to 64). Two sequences must not
+ * B * n * Hq rows and each of max_kv tokens (rounded up to 128). Two sequences must not
  * share a page here: both would write its weights. */
 size_t moe_attention_decode_weights_workspace_size(moe_attn_shape a, int32_t B, int32_t n,
                                                    int32_t max_kv);

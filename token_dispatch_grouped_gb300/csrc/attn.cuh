@@ -172,7 +172,7 @@ struct Decode {
     float* ws;
     int* err;
 };
-size_t decode_ws_floats(const moe_attn_shape& a, int B, int n, int max_kv, bool weights);
+size_t decode_ws_floats(const moe_attn_shape& a, int B, int n, int max_kv, bool e8, bool weights);
 cudaError_t launch_attention_decode(const Decode& p, cudaStream_t st);
 
 // ---------------------------------------------------------------- cache8.cu
@@ -218,6 +218,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair) {
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(pair)));
     return r;
+}
+// Four e4m3 values as two pairs in fp16.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
 }
 // Four e4m3 values times f, rounded to e4m3 again.
 __device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t v, float f) {

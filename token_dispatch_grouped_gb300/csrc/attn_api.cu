@@ -163,11 +163,12 @@ struct Pages {
     int pages, page_size, shift;
 };
 
-size_t decode_ws_bytes(const moe_attn_shape& a, int32_t B, int32_t n, int32_t max_kv, bool weights) {
+size_t decode_ws_bytes(const moe_attn_shape& a, int32_t B, int32_t n, int32_t max_kv, bool e8,
+                       bool weights) {
     if (check_attn(a) || B < 1 || n < 1 || max_kv < 1 || max_kv > kMaxCached ||
         static_cast<int64_t>(B) * n > kMaxTokens)
         return 0;
-    return sizeof(float) * decode_ws_floats(a, B, n, max_kv, weights);
+    return sizeof(float) * decode_ws_floats(a, B, n, max_kv, e8, weights);
 }
 
 int decode_of(const moe_attn_shape& a, int32_t B, int32_t n, int32_t max_kv, float scale, moe_heads q,
@@ -182,7 +183,7 @@ int decode_of(const moe_attn_shape& a, int32_t B, int32_t n, int32_t max_kv, flo
     ATTN_TRY(check_heads(&q, T, a.Hq, a.D, false));
     ATTN_TRY(check_heads(&out, T, a.Hq, a.D, true));
     ATTN_TRY(check_table(block_table, table_stride, kv_lens, max_kv, c.page_size));
-    const size_t need = decode_ws_bytes(a, B, n, max_kv, weights != nullptr);
+    const size_t need = decode_ws_bytes(a, B, n, max_kv, c.k_scale != nullptr, weights != nullptr);
     if (need > 0 && !ws) return MOE_ERR_INVALID_ARG;
     if (!aligned16(ws)) return MOE_ERR_MISALIGNED;
     if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
@@ -466,7 +467,7 @@ int moe_attention_backward(moe_attn_shape a, moe_packed s, float scale, moe_head
 
 size_t moe_attention_decode_workspace_size(moe_attn_shape a, int32_t B, int32_t n,
                                            int32_t max_kv) {
-    return decode_ws_bytes(a, B, n, max_kv, false);
+    return decode_ws_bytes(a, B, n, max_kv, false, false);
 }
 
 int moe_attention_decode(moe_attn_shape a, int32_t B, int32_t n, int32_t max_kv, float scale,
@@ -484,7 +485,7 @@ int moe_attention_decode(moe_attn_shape a, int32_t B, int32_t n, int32_t max_kv,
 
 size_t moe_attention_decode_weights_workspace_size(moe_attn_shape a, int32_t B, int32_t n,
                                                    int32_t max_kv) {
-    return decode_ws_bytes(a, B, n, max_kv, true);
+    return decode_ws_bytes(a, B, n, max_kv, false, true);
 }
 
 int moe_attention_decode_weights(moe_attn_shape a, int32_t B, int32_t n, int32_t max_kv,
@@ -504,7 +505,7 @@ int moe_attention_decode_weights(moe_attn_shape a, int32_t B, int32_t n, int32_t
 
 size_t moe_attention_decode8_workspace_size(moe_attn_shape a, int32_t B, int32_t n,
                                             int32_t max_kv, int32_t with_weights) {
-    return a.D % 16 != 0 ? 0 : decode_ws_bytes(a, B, n, max_kv, with_weights != 0);
+    return a.D % 16 != 0 ? 0 : decode_ws_bytes(a, B, n, max_kv, true, with_weights != 0);
 }
 
 int moe_attention_decode8(moe_attn_shape a, int32_t B, int32_t n, int32_t max_kv, float scale,

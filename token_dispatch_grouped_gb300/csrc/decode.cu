@@ -15,7 +15,7 @@
 // P is rounded to bf16 for its product; maxima, sums and O are fp32. Tokens past a row's
 // limit get weight 0 by selection; rows of V past the length are zeroed in shared memory,
 // whatever the page holds there.
-#include "attn_mma.cuh"
+#include "decode.cuh"
 
 namespace moe {
 namespace attn {
@@ -24,61 +24,18 @@ namespace {
 constexpr int kTokens = 64;   // of a stage
 constexpr int kWarps = 4;     // 16 tokens of a stage each
 constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kRowTile = 16;
-// E8: P enters its product in fp16 as weight * kLift, so that the many small weights beside one
-// that is near 1 keep their share (fp16 ends at 2^-24, a lifted weight at 2^-39).
-constexpr float kLift = 32768.f;
 
-// DP: D padded to 64 or 128; E8: pages of e4m3 values (else bf16). A row of a stage is one
-// box row: PIECES pieces of ROW bytes, swizzled over ROW bytes.
-template <int DP, bool E8>
+template <int DP>
 struct Cfg {
-    static constexpr int PIECES = E8 ? 1 : DP / 64;
-    static constexpr int ROW = E8 ? DP : 128;
-    static constexpr int HALF = PIECES * kTokens * ROW;  // K or V of a stage
+    static constexpr int PIECES = DP / 64;
+    static constexpr int HALF = PIECES * kTokens * 128;  // K or V of a stage
     static constexpr int STAGE = 2 * HALF;
-    static constexpr int STAGES = 98304 / STAGE;         // 96 KB: two CTAs an SM
-    static constexpr int BOXES = kTokens / 8;            // of a stage at most: pages of 8 tokens
-    static constexpr int SCALES = E8 ? STAGES * BOXES * 2 * 4 : 0;
-    static constexpr int SMEM =
-        1024 + STAGES * STAGE + 2 * kWarps * kRowTile * 4 + SCALES + 16 * STAGES + 16;
+    static constexpr int STAGES = DP == 128 ? 3 : 6;     // 96 KB: two CTAs an SM
+    static constexpr int SMEM = 1024 + STAGES * STAGE + 2 * kWarps * kRowTile * 4 + 256;
     static constexpr int PITCH = DP + 4;                 // floats of a merged row
     static_assert(kWarps * kRowTile * PITCH * 4 <= STAGES * STAGE, "merge area");
 };
 
-struct Params {
-    moe_attn_shape a;
-    int B, n, max_kv;
-    float scale;
-    Heads q, out;
-    int pages, page_shift;
-    const int32_t* table;
-    int table_stride;
-    const int32_t* lens;
-    float *part, *part_ml;  // [row][parts][D] and [row][parts][2] (row = token, head)
-    int parts, chunk;       // tokens of a part
-    int row_tiles;
-    int* err;
-    const float *k_scale, *v_scale;  // E8
-    float* scores;          // weights: [sequence][head][row of its G n][pitch], base 2, -inf unseen
-    float* lse;             // weights: [row], base 2, inf where nothing is seen
-    int pitch;
-    float* weights;
-    int fresh;
-};
-
-__device__ __forceinline__ void ldm4(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldm4t(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
 __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -87,37 +44,19 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void mma16h(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-// 16-byte chunk c of row r of an E8 stage, whose rows are swizzled over their DP bytes.
-template <int DP>
-__device__ __forceinline__ uint32_t chunk8(int r, int c) {
-    return r * DP + ((DP == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
-}
-
-// E8: pages of e4m3; W: scores and log-sum-exps are kept for weights_kernel.
-template <int DP, bool E8, bool W>
+// W: scores and log-sum-exps are kept for weights_kernel.
+template <int DP, bool W>
 __global__ void __launch_bounds__(kThreads, 2)
 decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
-              const Params p) {
-    using C = Cfg<DP, E8>;
+              const DecodeParams p) {
+    using C = Cfg<DP>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t* tail = smem_raw + (base - raw) + C::STAGES * C::STAGE;
     float* s_m = reinterpret_cast<float*>(tail);  // [warp][row]
     float* s_l = s_m + kWarps * kRowTile;
-    float* s_scale = s_l + kWarps * kRowTile;  // E8: [stage][K, V][box]
-    uint8_t* misc = tail + 2 * kWarps * kRowTile * 4 + C::SCALES;
+    uint8_t* misc = tail + 2 * kWarps * kRowTile * 4;
     const uint32_t bars = smem_u32(misc);
     const auto full = [&](int s) { return bars + 8u * s; };
     const auto empty = [&](int s) { return bars + 8u * (C::STAGES + s); };
@@ -160,60 +99,28 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
         // ---------------------------------------------------------------- pages
         const int* table = p.table + static_cast<long long>(b) * p.table_stride;
         const int sh = p.page_shift, rows = min(1 << sh, kTokens);  // of a box
-        // E8: the pages are looked up two stages ahead and their scales one, so that no load
-        // stands between a free slot and its boxes
-        const auto page_at = [&](int i) {
-            const int tok = t0 + i * kTokens + lane * rows;
-            return lane < kTokens / rows && tok < t1 ? table[tok >> sh] : -1;
-        };
-        const auto scales_of = [&](int page) {
-            if (page < 0 || page >= p.pages) return make_float2(0.f, 0.f);
-            const long long at = static_cast<long long>(page) * p.a.Hkv + hk;
-            return make_float2(p.k_scale[at], p.v_scale[at]);
-        };
-        int page0 = -1, page1 = -1;
-        float2 sc0 = make_float2(0.f, 0.f);
-        if constexpr (E8) {
-            page0 = page_at(0);
-            page1 = page_at(1);
-            sc0 = scales_of(page0);
-        }
         int i = 0;
         for (; i < stages; ++i) {
             const int slot = i % C::STAGES;
-            int page2 = -1;
-            float2 sc1 = make_float2(0.f, 0.f);
-            if constexpr (E8) {
-                page2 = page_at(i + 2);
-                sc1 = scales_of(page1);
-            }
             if (i >= C::STAGES) warp_wait(empty(slot), (i / C::STAGES - 1) & 1, abort_flag);
             if (__any_sync(~0u, *abort_flag != 0)) break;
             // box x of this stage: rows x * rows .. of K and V; lane x has its page
             const int tok = t0 + i * kTokens + lane * rows;
             const bool mine = lane < kTokens / rows && tok < t1;
-            const int page = E8 ? page0 : mine ? table[tok >> sh] : 0;
+            int page = mine ? table[tok >> sh] : 0;
             const bool bad = mine && (page < 0 || page >= p.pages);
             if (bad) raise_error(p.err, MOE_ERR_BAD_INDEX);
             const bool load = mine && !bad;
             const int boxes = __popc(__ballot_sync(~0u, load));
-            if constexpr (E8) {  // 0 for a box that is not there
-                if (lane < C::BOXES) {
-                    s_scale[(slot * 2) * C::BOXES + lane] = sc0.x;
-                    s_scale[(slot * 2 + 1) * C::BOXES + lane] = sc0.y;
-                }
-                __syncwarp();
-                page0 = page1, page1 = page2, sc0 = sc1;
-            }
-            if (lane == 0) mbar_arrive_expect_tx(full(slot), boxes * rows * C::ROW * C::PIECES * 2);
+            if (lane == 0) mbar_arrive_expect_tx(full(slot), boxes * rows * 128 * C::PIECES * 2);
             __syncwarp();
             if (load) {
                 const int y = ((page * p.a.Hkv + hk) << sh) + (tok & ((1 << sh) - 1));
-                const uint32_t dst = base + slot * C::STAGE + lane * rows * C::ROW;
+                const uint32_t dst = base + slot * C::STAGE + lane * rows * 128;
 #pragma unroll
                 for (int c = 0; c < C::PIECES; ++c) {
-                    tma_load_2d(dst + c * kTokens * C::ROW, &mapK, full(slot), 64 * c, y);
-                    tma_load_2d(dst + C::HALF + c * kTokens * C::ROW, &mapV, full(slot), 64 * c, y);
+                    tma_load_2d(dst + c * kTokens * 128, &mapK, full(slot), 64 * c, y);
+                    tma_load_2d(dst + C::HALF + c * kTokens * 128, &mapV, full(slot), 64 * c, y);
                 }
             }
             __syncwarp();
@@ -227,7 +134,6 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
         const int c2 = (lane & 3) * 2;
         uint32_t qa[DP / 16][4];
         int lim[2];
-        float c[2];  // what turns a row's product into its score, in powers of two
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int r = r0 + 8 * u;
@@ -239,43 +145,13 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
             for (int k = 0; k < DP / 16; ++k)
 #pragma unroll
                 for (int v = 0; v < 2; ++v) {
-                    // (E8: a lane's four bytes of a key row are four values in a row)
-                    const int col = 16 * k + (E8 ? 2 * c2 + 2 * v : 8 * v + c2);
+                    const int col = 16 * k + 8 * v + c2;
                     qa[k][2 * v + u] = valid && col < D ? *reinterpret_cast<const uint32_t*>(src + col) : 0u;
                 }
-            c[u] = p.scale * 1.44269504088896341f;
-            if constexpr (E8) {
-                // The row in fp16: divided by the power of two that brings its largest value to
-                // [1, 2), where bf16 values down to 2^-17 of the largest are exact and the
-                // others off by at most 2^-25 of it.
-                uint32_t top = 0;
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        const uint32_t w = qa[k][2 * v + u] & 0x7fff7fffu;
-                        top = max(top, max(w & 0xffffu, w >> 16));
-                    }
-                top = max(top, __shfl_xor_sync(~0u, top, 1));
-                top = max(top, __shfl_xor_sync(~0u, top, 2));
-                const int e = min(253, max(1, static_cast<int>(top >> 7)));  // the exponent's field
-                const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-                c[u] *= __uint_as_float(static_cast<uint32_t>(e) << 23);
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        const uint32_t w = qa[k][2 * v + u];
-                        qa[k][2 * v + u] = half2_of(__uint_as_float(w << 16) * inv,
-                                                    __uint_as_float(w & 0xffff0000u) * inv);
-                    }
-            }
         }
         // the tokens before this one are seen by every row
         const int open = len - p.n + 1;
-        // E8: O is summed in units of vr, the largest value scale so far
-        float vr = 0.f, vr_inv = 0.f;
-        const int box_shift = min(p.page_shift, 6);
+        const float c = p.scale * 1.44269504088896341f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
         float o[DP / 8][4];
 #pragma unroll
@@ -287,27 +163,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
             if (tok < t1) {
                 const uint32_t sK = base + slot * C::STAGE, sV = sK + C::HALF;
                 float s[2][4] = {};
-                float ks[2], vs[2];  // E8: scales of the two groups of 8 tokens
-                if constexpr (E8) {
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int box = (16 * warp + 8 * t) >> box_shift;
-                        ks[t] = s_scale[(slot * 2) * C::BOXES + box];
-                        vs[t] = s_scale[(slot * 2 + 1) * C::BOXES + box];
-                    }
-                    // a chunk of 16 bytes is 16 of K: lane i of a row's four holds values 4 i ..
-                    // 4 i + 3, two for each half of the fragment
-                    const int row = 16 * warp + (lane >> 4) * 8 + (lane & 7), half = (lane >> 3) & 1;
-#pragma unroll
-                    for (int k = 0; k < DP / 16; k += 2) {
-                        uint32_t kb[4];
-                        ldm4(sK + chunk8<DP>(row, k + half), kb);
-                        mma16h(s[0], qa[k], e4m3x2_to_f16x2(kb[0]), e4m3x2_to_f16x2(kb[0] >> 16));
-                        mma16h(s[1], qa[k], e4m3x2_to_f16x2(kb[2]), e4m3x2_to_f16x2(kb[2] >> 16));
-                        mma16h(s[0], qa[k + 1], e4m3x2_to_f16x2(kb[1]), e4m3x2_to_f16x2(kb[1] >> 16));
-                        mma16h(s[1], qa[k + 1], e4m3x2_to_f16x2(kb[3]), e4m3x2_to_f16x2(kb[3] >> 16));
-                    }
-                } else {
+                {
                     const int row = 16 * warp + (lane >> 4) * 8 + (lane & 7), half = (lane >> 3) & 1;
 #pragma unroll
                     for (int k = 0; k < DP / 16; ++k) {
@@ -322,7 +178,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[t][e] *= E8 ? c[e >> 1] * ks[t] : c[e >> 1];
+                    for (int e = 0; e < 4; ++e) s[t][e] *= c;
                 if (tok + 16 > open || tok + 16 > t1) {
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
@@ -331,13 +187,11 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
                             if (tok + 8 * t + c2 + (e & 1) >= min(t1, lim[e >> 1])) s[t][e] = -INFINITY;
                     // rows of V past the length hold whatever the page held
                     if (tok + 16 > t1) {
-                        constexpr int CH = C::ROW / 16;
-                        for (int x = lane; x < 16 * CH * C::PIECES; x += 32) {
-                            const int row = 16 * warp + (x / CH) % 16;
+                        for (int x = lane; x < 16 * 8 * C::PIECES; x += 32) {
+                            const int row = 16 * warp + (x >> 3) % 16;
                             if (t0 + i * kTokens + row >= t1)
                                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                                 sV + x / (16 * CH) * kTokens * C::ROW + row * C::ROW +
-                                                 (x % CH) * 16),
+                                                 sV + (x >> 7) * kTokens * 128 + row * 128 + (x & 7) * 16),
                                              "r"(0)
                                              : "memory");
                         }
@@ -355,20 +209,6 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
                             *reinterpret_cast<float2*>(dst + 8 * t) =
                                 make_float2(s[t][2 * u], s[t][2 * u + 1]);
                     }
-                }
-                if constexpr (E8) {  // the same in every lane
-                    const float vn = fmaxf(vr, fmaxf(vs[0], vs[1]));
-                    if (vn > vr) {
-                        vr_inv = 1.f / vn;
-                        const float f = vr * vr_inv;
-                        vr = vn;
-#pragma unroll
-                        for (int d = 0; d < DP / 8; ++d)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) o[d][e] *= f;
-                    }
-                    vs[0] *= vr_inv * kLift;
-                    vs[1] *= vr_inv * kLift;
                 }
                 uint32_t pa[4];
                 bool grew = false;
@@ -402,27 +242,9 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
                         const float x = exp2_fast(s[t][2 * u] - base2[u]);
                         const float y = exp2_fast(s[t][2 * u + 1] - base2[u]);
                         l[u] += x + y;
-                        pa[2 * t + u] = E8 ? half2_of(x * vs[t], y * vs[t]) : pack2(x, y);
+                        pa[2 * t + u] = pack2(x, y);
                     }
                 const int row = 16 * warp + ((lane >> 3) & 1) * 8 + (lane & 7), half = lane >> 4;
-                if constexpr (E8) {
-                    // a transposed pair of bytes is two columns of two tokens: sorted by column,
-                    // each pair feeds the product of the even and of the odd columns of a chunk
-#pragma unroll
-                    for (int d = 0; d < DP / 16; d += 2) {
-                        uint32_t vb[4];
-                        ldm4t(sV + chunk8<DP>(row, d + half), vb);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) vb[j] = __byte_perm(vb[j], 0u, 0x3120);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            mma16h(o[2 * (d + j)], pa, e4m3x2_to_f16x2(vb[2 * j]),
-                                   e4m3x2_to_f16x2(vb[2 * j + 1]));
-                            mma16h(o[2 * (d + j) + 1], pa, e4m3x2_to_f16x2(vb[2 * j] >> 16),
-                                   e4m3x2_to_f16x2(vb[2 * j + 1] >> 16));
-                        }
-                    }
-                } else
 #pragma unroll
                 for (int d = 0; d < DP / 16; ++d) {
                     uint32_t vb[4];
@@ -451,19 +273,10 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
                 s_m[warp * kRowTile + r] = m[u];
                 s_l[warp * kRowTile + r] = l[u];
             }
-            float* dst = merge + (warp * kRowTile + r) * C::PITCH;
-            if constexpr (E8) {  // even and odd columns of a chunk: four in a row
-                const float f = vr * (1.f / kLift);
 #pragma unroll
-                for (int d = 0; d < DP / 16; ++d)
-                    *reinterpret_cast<float4*>(dst + 16 * d + 2 * c2) =
-                        make_float4(o[2 * d][2 * u] * f, o[2 * d + 1][2 * u] * f,
-                                    o[2 * d][2 * u + 1] * f, o[2 * d + 1][2 * u + 1] * f);
-            } else {
-#pragma unroll
-                for (int d = 0; d < DP / 8; ++d)
-                    *reinterpret_cast<float2*>(dst + 8 * d + c2) = make_float2(o[d][2 * u], o[d][2 * u + 1]);
-            }
+            for (int d = 0; d < DP / 8; ++d)
+                *reinterpret_cast<float2*>(merge + (warp * kRowTile + r) * C::PITCH + 8 * d + c2) =
+                    make_float2(o[d][2 * u], o[d][2 * u + 1]);
         }
         asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
         // 8 threads a row, each a run of columns in steps of 8 x 4
@@ -517,7 +330,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ 
 }
 
 // Joins the parts of each row, in part order: one warp a row, four columns a lane.
-__global__ void __launch_bounds__(128) join_kernel(const Params p) {
+__global__ void __launch_bounds__(128) join_kernel(const DecodeParams p) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
@@ -573,7 +386,7 @@ __global__ void __launch_bounds__(128) join_kernel(const Params p) {
 // Adds up the weights of every cached token and key/value head from the kept scores: four
 // tokens a thread, their rows in order. 4 (G n + 2) bytes a token and head against the 4 D (2 D
 // for e4m3) that the decode kernel reads for it.
-__global__ void __launch_bounds__(256) weights_kernel(const Params p, int blocks) {
+__global__ void __launch_bounds__(256) weights_kernel(const DecodeParams p, int blocks) {
     pdl_wait();
     pdl_trigger();
     if (__syncthreads_or(stopped(p.err))) return;
@@ -604,113 +417,105 @@ __global__ void __launch_bounds__(256) weights_kernel(const Params p, int blocks
         if (t + e < len) dst[e] = (p.fresh || t + e >= len - p.n ? 0.f : dst[e]) + w[e];
 }
 
+template <int DP, bool W>
+cudaError_t decode(const Decode& d, cudaStream_t st) {
+    using C = Cfg<DP>;
+    const DecodePlan pl = decode_plan(d.a, d.B, d.n, d.max_kv, false);
+    const long long items = static_cast<long long>(d.B) * d.a.Hkv * pl.parts * pl.row_tiles;
+    if (items > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    const DecodeParams p = decode_params(d, pl);
+    CUtensorMap mk, mv;
+    const uint64_t cache_rows = (static_cast<uint64_t>(d.pages) * d.a.Hkv) << d.page_shift;
+    const uint32_t box = (1 << d.page_shift) < kTokens ? (1 << d.page_shift) : kTokens;
+    if (!make_tmap_bf16(&mk, d.k_pages, cache_rows, d.a.D, 64, box) ||
+        !make_tmap_bf16(&mv, d.v_pages, cache_rows, d.a.D, 64, box))
+        return cudaErrorInvalidValue;
+    auto kfn = decode_kernel<DP, W>;
+    cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    {
+        LaunchScope ls("attention_decode", st);
+        e = launch_pdl(kfn, dim3(static_cast<unsigned>(items)), dim3(kThreads), C::SMEM, st, mk, mv, p);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_decode_rest(p, st);
+}
+
+}  // namespace
+
 // Tokens of a part: about eight parts for every CTA that the GPU holds at once, so that
 // uneven sequences even out, between 128 tokens (two stages, below which the merge costs
 // more than the reads) and 2048 (where writing and reading the partial results of one tile of
 // 16 rows moves under 2% of the bytes that the part reads; each further row tile adds as much,
 // while its cache reads come from L2).
-struct Plan {
-    int chunk, parts, row_tiles;
-};
-Plan plan_of(const moe_attn_shape& a, int B, int n, int max_kv) {
+DecodePlan decode_plan(const moe_attn_shape& a, int B, int n, int max_kv, bool e8) {
+    const int stage = e8 ? 128 : kTokens;
     const int row_tiles = (a.Hq / a.Hkv * n + kRowTile - 1) / kRowTile;
     const long long tokens = static_cast<long long>(B) * a.Hkv * row_tiles * max_kv;
     long long chunk = tokens / (static_cast<long long>(num_sms()) * 2 * 8);
     chunk = chunk < 128 ? 128 : chunk > 2048 ? 2048 : chunk;
-    chunk = (chunk + kTokens - 1) / kTokens * kTokens;
+    chunk = (chunk + stage - 1) / stage * stage;
     const long long parts = max_kv > 0 ? (max_kv + chunk - 1) / chunk : 1;
     return {static_cast<int>(chunk), static_cast<int>(parts), row_tiles};
 }
 
-// The workspace: partial results of the parts, then what the weights are summed from.
-struct Space {
-    size_t part, lse, scores, total;  // in floats; each a multiple of 4
-    int pitch;
-};
-Space space_of(const moe_attn_shape& a, int B, int n, int max_kv, const Plan& pl, bool weights) {
+DecodeSpace decode_space(const Decode& d, const DecodePlan& pl) {
     const auto up = [](size_t x) { return (x + 3) / 4 * 4; };
-    const size_t rows = static_cast<size_t>(B) * n * a.Hq;
-    Space s{};
-    s.part = pl.parts == 1 ? 0 : up(rows * pl.parts * (a.D + 2));
-    s.pitch = (max_kv + kTokens - 1) / kTokens * kTokens;
+    const size_t rows = static_cast<size_t>(d.B) * d.n * d.a.Hq;
+    const bool weights = d.weights != nullptr;
+    DecodeSpace s{};
+    s.part = pl.parts == 1 ? 0 : up(rows * pl.parts * (d.a.D + 2));
+    s.pitch = (d.max_kv + 127) / 128 * 128;  // whole stages
     s.lse = weights ? up(rows) : 0;
     s.scores = weights ? rows * s.pitch : 0;
     s.total = s.part + s.lse + s.scores;
+    if (d.k_scale != nullptr && decode_numbered(d.a, d.B, pl)) s.total += 4;  // the count
     return s;
 }
 
-// Tensor map of e4m3 rows [rows, cols] with a box of `box_cols` (64 or 128, its swizzle) x box_rows.
-bool make_tmap_e4m3(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint32_t box_cols,
-                    uint32_t box_rows) {
-    auto fn = tensor_map_encoder();
-    if (fn == nullptr) return false;
-    cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {cols};
-    cuuint32_t box[2] = {box_cols, box_rows};
-    cuuint32_t es[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE,
-              box_cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+DecodeParams decode_params(const Decode& d, const DecodePlan& pl) {
+    const DecodeSpace sp = decode_space(d, pl);
+    const size_t rows = static_cast<size_t>(d.B) * d.n * d.a.Hq;
+    const bool w = d.weights != nullptr;
+    return {d.a, d.B, d.n, d.max_kv, d.scale, d.q, d.out, d.pages, d.page_shift, d.block_table,
+            d.table_stride, d.kv_lens, d.ws, pl.parts == 1 ? nullptr : d.ws + rows * pl.parts * d.a.D,
+            pl.parts, pl.chunk, pl.row_tiles, d.err, d.k_scale, d.v_scale,
+            w ? d.ws + sp.part + sp.lse : nullptr, w ? d.ws + sp.part : nullptr, sp.pitch, d.weights,
+            d.fresh};
 }
 
-template <int DP, bool E8, bool W>
-cudaError_t decode(const Decode& d, cudaStream_t st) {
-    using C = Cfg<DP, E8>;
-    const Plan pl = plan_of(d.a, d.B, d.n, d.max_kv);
-    const Space sp = space_of(d.a, d.B, d.n, d.max_kv, pl, W);
-    const long long rows = static_cast<long long>(d.B) * d.n * d.a.Hq;
-    const long long items = static_cast<long long>(d.B) * d.a.Hkv * pl.parts * pl.row_tiles;
-    const int blocks = (d.max_kv + 1023) / 1024;
-    const long long weight_items = static_cast<long long>(d.B) * d.a.Hkv * blocks;
-    if (items > 0x7fffffffll || (W && weight_items > 0x7fffffffll)) return cudaErrorInvalidConfiguration;
-    const Params p{d.a, d.B, d.n, d.max_kv, d.scale, d.q, d.out, d.pages, d.page_shift, d.block_table,
-                   d.table_stride, d.kv_lens, d.ws, d.ws + rows * pl.parts * d.a.D, pl.parts,
-                   pl.chunk, pl.row_tiles, d.err, d.k_scale, d.v_scale,
-                   W ? d.ws + sp.part + sp.lse : nullptr, W ? d.ws + sp.part : nullptr, sp.pitch,
-                   d.weights, d.fresh};
-    CUtensorMap mk, mv;
-    const uint64_t cache_rows = (static_cast<uint64_t>(d.pages) * d.a.Hkv) << d.page_shift;
-    const uint32_t box = (1 << d.page_shift) < kTokens ? (1 << d.page_shift) : kTokens;
-    const bool ok = E8 ? make_tmap_e4m3(&mk, d.k_pages, cache_rows, d.a.D, DP, box) &&
-                             make_tmap_e4m3(&mv, d.v_pages, cache_rows, d.a.D, DP, box)
-                       : make_tmap_bf16(&mk, d.k_pages, cache_rows, d.a.D, 64, box) &&
-                             make_tmap_bf16(&mv, d.v_pages, cache_rows, d.a.D, 64, box);
-    if (!ok) return cudaErrorInvalidValue;
-    auto kfn = decode_kernel<DP, E8, W>;
-    cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    {
-        LaunchScope ls(E8 ? "attention_decode8" : "attention_decode", st);
-        e = launch_pdl(kfn, dim3(static_cast<unsigned>(items)), dim3(kThreads), C::SMEM, st, mk, mv, p);
-        if (e != cudaSuccess) return e;
-    }
-    if (pl.parts > 1) {
+cudaError_t launch_decode_rest(const DecodeParams& p, cudaStream_t st) {
+    const long long rows = static_cast<long long>(p.B) * p.n * p.a.Hq;
+    if (p.parts > 1) {
         LaunchScope ls("attention_join", st);
-        e = launch_pdl(join_kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, st, p);
+        const cudaError_t e = launch_pdl(join_kernel, dim3(static_cast<unsigned>((rows + 3) / 4)),
+                                         dim3(128), 0, st, p);
         if (e != cudaSuccess) return e;
     }
-    if (!W || blocks == 0) return e;
+    const int blocks = (p.max_kv + 1023) / 1024;
+    if (p.weights == nullptr || blocks == 0) return cudaSuccess;
+    const long long items = static_cast<long long>(p.B) * p.a.Hkv * blocks;
+    if (items > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     LaunchScope ls("attention_weights", st);
-    return launch_pdl(weights_kernel, dim3(static_cast<unsigned>(weight_items)), dim3(256), 0, st, p,
-                      blocks);
+    return launch_pdl(weights_kernel, dim3(static_cast<unsigned>(items)), dim3(256), 0, st, p, blocks);
 }
 
-template <int DP, bool E8>
-cudaError_t decode_w(const Decode& p, cudaStream_t st) {
-    return p.weights != nullptr ? decode<DP, E8, true>(p, st) : decode<DP, E8, false>(p, st);
-}
-
-}  // namespace
-
-size_t decode_ws_floats(const moe_attn_shape& a, int B, int n, int max_kv, bool weights) {
-    return space_of(a, B, n, max_kv, plan_of(a, B, n, max_kv), weights).total;
+size_t decode_ws_floats(const moe_attn_shape& a, int B, int n, int max_kv, bool e8, bool weights) {
+    Decode d{};
+    d.a = a;
+    d.B = B;
+    d.n = n;
+    d.max_kv = max_kv;
+    float any;
+    d.weights = weights ? &any : nullptr;
+    d.k_scale = e8 ? &any : nullptr;
+    return decode_space(d, decode_plan(a, B, n, max_kv, e8)).total;
 }
 
 cudaError_t launch_attention_decode(const Decode& p, cudaStream_t st) {
-    if (p.k_scale != nullptr)
-        return p.a.D <= 64 ? decode_w<64, true>(p, st) : decode_w<128, true>(p, st);
-    return p.a.D <= 64 ? decode_w<64, false>(p, st) : decode_w<128, false>(p, st);
+    if (p.k_scale != nullptr) return launch_decode8(p, st);
+    if (p.weights != nullptr) return p.a.D <= 64 ? decode<64, true>(p, st) : decode<128, true>(p, st);
+    return p.a.D <= 64 ? decode<64, false>(p, st) : decode<128, false>(p, st);
 }
 
 }  // namespace attn
