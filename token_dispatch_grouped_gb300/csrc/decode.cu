@@ -44,7 +44,7 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// W: scores and log-sum-exps are kept for weights_kernel.
+// W: scores are kept for weights_kernel.
 template <int DP, bool W>
 __global__ void __launch_bounds__(kThreads, 2)
 decode_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
@@ -383,38 +383,91 @@ __global__ void __launch_bounds__(128) join_kernel(const DecodeParams p) {
     }
 }
 
-// Adds up the weights of every cached token and key/value head from the kept scores: four
-// tokens a thread, their rows in order. 4 (G n + 2) bytes a token and head against the 4 D (2 D
-// for e4m3) that the decode kernel reads for it.
-__global__ void __launch_bounds__(256) weights_kernel(const DecodeParams p, int blocks) {
+// The sums of the weights of every cached token and key/value head from the kept scores:
+// 4 (G n + 2) bytes a token and head are moved, against the 4 D (2 D for e4m3) that the decode
+// kernel reads for it. A warp takes 128 tokens, four a lane, and the rows that are `split` modulo
+// `splits` of their sequence and head, four rows' loads in flight; the splits are added in their
+// order. (One row's load at a time: 55 us instead of MEASURED for 1.07 million tokens of 8 heads
+// of 4 rows. With the log-sum-exps formed here, so that the join could run beside it, 100 us.)
+constexpr int kSumWarps = 8;
+template <int RUN>
+__global__ void __launch_bounds__(kSumWarps * 32)
+weights_kernel(const DecodeParams p, int tiles, int splits) {
+    __shared__ float4 s_sum[kSumWarps][RUN][32];
     pdl_wait();
     pdl_trigger();
-    if (__syncthreads_or(stopped(p.err))) return;
-    long long item = blockIdx.x;
-    const int t = (static_cast<int>(item % blocks) * 256 + static_cast<int>(threadIdx.x)) * 4;
-    item /= blocks;
-    const int hk = static_cast<int>(item % p.a.Hkv), b = static_cast<int>(item / p.a.Hkv);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int split = warp % splits;
+    const int tile = static_cast<int>(blockIdx.x % tiles) * (kSumWarps / splits * RUN * 128);
+    const int t0 = tile + warp / splits * (RUN * 128) + lane * 4;  // and 128 further each time
+    const int unit = static_cast<int>(blockIdx.x / tiles), hk = unit % p.a.Hkv, b = unit / p.a.Hkv;
     const int len = p.lens[b];
-    if (len < 0 || len > p.max_kv || t >= len) return;
+    if (__syncthreads_or(stopped(p.err)) || len < 0 || len > p.max_kv || tile >= len) return;
     const int G = p.a.Hq / p.a.Hkv, R = G * p.n;
-    const int page = p.table[static_cast<long long>(b) * p.table_stride + (t >> p.page_shift)];
-    if (page < 0 || page >= p.pages) return;  // reported by the decode kernel
-    const float* src = p.scores + static_cast<long long>(b * p.a.Hkv + hk) * R * p.pitch + t;
-    const float* lse = p.lse + static_cast<long long>(b) * p.n * p.a.Hq + hk * G;
-    float w[4] = {};
-    for (int r = 0; r < R; ++r) {
-        const float4 x = *reinterpret_cast<const float4*>(src + static_cast<long long>(r) * p.pitch);
-        const float l = lse[static_cast<long long>(r / G) * p.a.Hq + r % G];
-        w[0] += exp2_fast(x.x - l);
-        w[1] += exp2_fast(x.y - l);
-        w[2] += exp2_fast(x.z - l);
-        w[3] += exp2_fast(x.w - l);
-    }
-    float* dst = p.weights + ((static_cast<long long>(page) * p.a.Hkv + hk) << p.page_shift) +
-                 (t & ((1 << p.page_shift) - 1));
+    int page[RUN];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (t + e < len) dst[e] = (p.fresh || t + e >= len - p.n ? 0.f : dst[e]) + w[e];
+    for (int k = 0; k < RUN; ++k) {
+        const int t = t0 + 128 * k;
+        page[k] = t < len && split == 0 ? p.table[static_cast<long long>(b) * p.table_stride + (t >> p.page_shift)]
+                                        : -1;
+        if (page[k] >= p.pages) page[k] = -1;  // reported by the decode kernel
+    }
+    const float* src = p.scores + static_cast<long long>(unit) * R * p.pitch + t0;
+    const float* lse = p.lse + static_cast<long long>(b) * p.n * p.a.Hq + hk * G;
+    float w[RUN][4] = {};
+    for (int r0 = split; r0 < R; r0 += 4 * splits) {
+        float4 x[4][RUN];
+        float l[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = r0 + j * splits;
+            l[j] = r < R ? lse[static_cast<long long>(r / G) * p.a.Hq + r % G] : INFINITY;
+#pragma unroll
+            for (int k = 0; k < RUN; ++k)
+                x[j][k] = r < R && t0 + 128 * k < len
+                              ? *reinterpret_cast<const float4*>(src + static_cast<long long>(r) * p.pitch + 128 * k)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < RUN; ++k) {
+                w[k][0] += exp2_fast(x[j][k].x - l[j]);
+                w[k][1] += exp2_fast(x[j][k].y - l[j]);
+                w[k][2] += exp2_fast(x[j][k].z - l[j]);
+                w[k][3] += exp2_fast(x[j][k].w - l[j]);
+            }
+    }
+    if (splits > 1) {
+#pragma unroll
+        for (int k = 0; k < RUN; ++k)
+            s_sum[warp][k][lane] = make_float4(w[k][0], w[k][1], w[k][2], w[k][3]);
+        __syncthreads();
+        if (split != 0) return;
+        for (int i = 1; i < splits; ++i)
+#pragma unroll
+            for (int k = 0; k < RUN; ++k) {
+                const float4 y = s_sum[warp + i][k][lane];
+                w[k][0] += y.x, w[k][1] += y.y, w[k][2] += y.z, w[k][3] += y.w;
+            }
+    }
+    const int old = p.fresh ? 0 : len - p.n;  // tokens before it had a sum
+#pragma unroll
+    for (int k = 0; k < RUN; ++k) {
+        if (page[k] < 0) continue;
+        const int t = t0 + 128 * k;
+        float* dst = p.weights + ((static_cast<long long>(page[k]) * p.a.Hkv + hk) << p.page_shift) +
+                     (t & ((1 << p.page_shift) - 1));
+        if (t + 4 <= old) {
+            const float4 y = *reinterpret_cast<const float4*>(dst);
+            *reinterpret_cast<float4*>(dst) =
+                make_float4(y.x + w[k][0], y.y + w[k][1], y.z + w[k][2], y.w + w[k][3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (t + e < len) dst[e] = (t + e < old ? dst[e] : 0.f) + w[k][e];
+        }
+    }
 }
 
 template <int DP, bool W>
@@ -478,7 +531,7 @@ DecodeParams decode_params(const Decode& d, const DecodePlan& pl) {
     const size_t rows = static_cast<size_t>(d.B) * d.n * d.a.Hq;
     const bool w = d.weights != nullptr;
     return {d.a, d.B, d.n, d.max_kv, d.scale, d.q, d.out, d.pages, d.page_shift, d.block_table,
-            d.table_stride, d.kv_lens, d.ws, pl.parts == 1 ? nullptr : d.ws + rows * pl.parts * d.a.D,
+            d.table_stride, d.kv_lens, d.ws, sp.part > 0 ? d.ws + rows * pl.parts * d.a.D : nullptr,
             pl.parts, pl.chunk, pl.row_tiles, d.err, d.k_scale, d.v_scale,
             w ? d.ws + sp.part + sp.lse : nullptr, w ? d.ws + sp.part : nullptr, sp.pitch, d.weights,
             d.fresh};
@@ -492,12 +545,17 @@ cudaError_t launch_decode_rest(const DecodeParams& p, cudaStream_t st) {
                                          dim3(128), 0, st, p);
         if (e != cudaSuccess) return e;
     }
-    const int blocks = (p.max_kv + 1023) / 1024;
-    if (p.weights == nullptr || blocks == 0) return cudaSuccess;
-    const long long items = static_cast<long long>(p.B) * p.a.Hkv * blocks;
-    if (items > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    if (p.weights == nullptr || p.max_kv == 0) return cudaSuccess;
+    const int R = p.a.Hq / p.a.Hkv * p.n;
+    const int splits = R > 16 ? 8 : R > 8 ? 4 : R > 4 ? 2 : 1;
+    const int run = kSumWarps / splits * 128;
+    const long long heads = static_cast<long long>(p.B) * p.a.Hkv;
+    const bool four = heads * (p.max_kv / (4 * run)) >= 4 * num_sms();
+    const int of = four ? 4 * run : run, tiles = (p.max_kv + of - 1) / of;
+    if (heads * tiles > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     LaunchScope ls("attention_weights", st);
-    return launch_pdl(weights_kernel, dim3(static_cast<unsigned>(items)), dim3(256), 0, st, p, blocks);
+    return launch_pdl(four ? weights_kernel<4> : weights_kernel<1>, dim3(static_cast<unsigned>(heads * tiles)),
+                      dim3(kSumWarps * 32), 0, st, p, tiles, splits);
 }
 
 size_t decode_ws_floats(const moe_attn_shape& a, int B, int n, int max_kv, bool e8, bool weights) {

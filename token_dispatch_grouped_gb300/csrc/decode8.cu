@@ -103,7 +103,7 @@ __device__ __forceinline__ bool item_of(const DecodeParams& p, const int* first,
     return true;
 }
 
-// W: scores and log-sum-exps are kept for the weights.
+// W: scores are kept for the weights.
 template <int DP, int NB, bool W>
 __global__ void __launch_bounds__(kThreads, 2)
 decode8_kernel(const __grid_constant__ CUtensorMap mapK, const __grid_constant__ CUtensorMap mapV,
