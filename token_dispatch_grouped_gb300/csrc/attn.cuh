@@ -206,36 +206,52 @@ cudaError_t launch_evict(const Evict& p, cudaStream_t st);
 __device__ __forceinline__ float finite_or_nan(float x) {
     return fabsf(x) <= 3.402823466e+38f ? x : __int_as_float(0x7fffffff);
 }
-__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+__device__ __forceinline__ uint32_t round_e4m3x2(float lo, float hi) {  // NaN stays; no infinities
     uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-        : "=h"(r)
-        : "f"(finite_or_nan(hi)), "f"(finite_or_nan(lo)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// The two values of e4m3 pairs in fp16 (exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t pair) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(pair)));
-    return r;
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+    return round_e4m3x2(finite_or_nan(lo), finite_or_nan(hi));
 }
-// Four e4m3 values as two pairs in fp16.
+// Four e4m3 values as two pairs in fp16 (exact).
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
         "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
         : "=r"(lo), "=r"(hi)
         : "r"(v));
 }
-// Four e4m3 values times f, rounded to e4m3 again.
-__device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t v, float f) {
-    uint32_t out = 0;
+// 16 e4m3 values times f <= 1, rounded to e4m3 again. By a power of two the product is formed in
+// fp16: exact from 2^-11 up, and everything below rounds to zero either way.
+__device__ __forceinline__ uint4 rescale_e4m3x16(const uint4& v, float f) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if ((__float_as_uint(f) & 0x7fffffu) == 0) {
+        const __half2 f2 = __float2half2_rn(f);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t h = e4m3x2_to_f16x2(v >> (16 * i));
-        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        out |= to_e4m3x2(x.x * f, x.y * f) << (16 * i);
+        for (int i = 0; i < 4; ++i) {
+            uint32_t h[2];
+            e4m3x4_to_f16(w[i], h[0], h[1]);
+            uint16_t r[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[j]), f2);
+                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
+                    : "=h"(r[j])
+                    : "r"(*reinterpret_cast<const uint32_t*>(&y)));
+            }
+            w[i] = static_cast<uint32_t>(r[0]) | static_cast<uint32_t>(r[1]) << 16;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t lo, hi;
+            e4m3x4_to_f16(w[i], lo, hi);
+            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+            w[i] = round_e4m3x2(x.x * f, x.y * f) | round_e4m3x2(y.x * f, y.y * f) << 16;
+        }
     }
-    return out;
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 }  // namespace attn

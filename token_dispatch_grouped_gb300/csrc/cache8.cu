@@ -152,12 +152,7 @@ __global__ void __launch_bounds__(kWarps * 32) append8_kernel(const Append8 p) {
         const float f = old / scale;
         for (int i = threadIdx.x; i < o * (D / 16); i += kWarps * 32) {
             uint4* at = reinterpret_cast<uint4*>(dst) + i;
-            uint4 v = *at;
-            v.x = rescale_e4m3x4(v.x, f);
-            v.y = rescale_e4m3x4(v.y, f);
-            v.z = rescale_e4m3x4(v.z, f);
-            v.w = rescale_e4m3x4(v.w, f);
-            *at = v;
+            *at = rescale_e4m3x16(*at, f);
         }
     } else if (o == 0 && threadIdx.x == 0) {
         *scale_at = scale;

@@ -1,12 +1,14 @@
 // evict.cu — the tokens of each sequence and key/value head that a cache keeps, and their way
 // into other pages.
 //
-// select_kernel, a CTA for each (sequence, head): the m-th largest of the weights that compete
-// by a radix select over their bits as ordered whole numbers (8 bits a pass), then the kept
-// tokens' places in order, by running counts of the tokens above that weight and of those that
-// have just that (the first of them are kept). gather_kernel, a CTA for each new page of a
-// head: its rows from their old pages, 2 x 2 D bytes (D for e4m3) read and written a token;
-// with e4m3 pages the new scale is the largest of the rows' and the others are moved to it.
+// select_kernel, a CTA for each (sequence, head): the weights that compete are read once, as
+// whole numbers in their order, into shared memory (again from the pages at every use where a
+// sequence is longer than that holds); the m-th largest by a radix select in three passes of 11,
+// 11 and 10 bits; then the kept tokens' places in order: each warp counts, and then writes, those
+// of a run of its own that are above that weight, and the first of those that have just that.
+// gather_kernel, a CTA for each new page of a head: its rows from their old pages, 2 x 2 D bytes
+// (D for e4m3) read and written a token; with e4m3 pages the new scale is the largest of the rows'
+// and the others are moved to it.
 #include "attn.cuh"
 
 namespace moe {
@@ -23,35 +25,28 @@ __device__ __forceinline__ uint32_t key_of(float w) {
     return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
-// Tokens before this thread's whose flag is set, and the block's sum (every thread calls).
-__device__ __forceinline__ int count_before(bool flag, int* s_warp, int& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned votes = __ballot_sync(~0u, flag);
-    __syncthreads();
-    if (lane == 0) s_warp[warp] = __popc(votes);
-    __syncthreads();
-    int before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kSelect / 32; ++w) {
-        const int c = s_warp[w];
-        before += w < warp ? c : 0;
-        total += c;
-    }
-    return before + __popc(votes & ((1u << lane) - 1));
-}
+constexpr int kBins = 2048;
+constexpr int kHeld = 48 * 1024;  // weights in shared memory at most: 192 KB
 
-__global__ void __launch_bounds__(kSelect) select_kernel(const Evict p) {
-    __shared__ int s_hist[256];
+// How many of a warp's keys are above `last`, or at it; from `t` to `end` in steps of 32.
+struct Count {
+    int more, same;
+};
+
+// HELD: keys in shared memory.
+template <bool HELD>
+__global__ void __launch_bounds__(kSelect, 2) select_kernel(const Evict p) {
+    extern __shared__ uint32_t s_key[];
+    __shared__ int s_bins[kBins];
     __shared__ int s_warp[kSelect / 32];
-    __shared__ uint32_t s_digit;
-    __shared__ int s_left;
+    __shared__ Count s_count[kSelect / 32];
+    __shared__ int s_digit, s_left;
     pdl_wait();
     pdl_trigger();
-    if (__syncthreads_or(stopped(p.err))) return;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int hk = blockIdx.x % p.Hkv, b = blockIdx.x / p.Hkv;
     const int len = p.lens[b], sh = p.page_shift;
+    if (__syncthreads_or(stopped(p.err))) return;
     int* kept = p.kept + static_cast<long long>(blockIdx.x) * p.keep;
     const bool bad = len < 0 || len > p.max_kv;
     if (bad && tid == 0) raise_error(p.err, MOE_ERR_BAD_INDEX);
@@ -59,8 +54,11 @@ __global__ void __launch_bounds__(kSelect) select_kernel(const Evict p) {
         for (int i = tid; i < p.keep; i += kSelect) kept[i] = !bad && i < len ? i : -1;
         return;
     }
+    const int rivals = len - p.recent, m = p.keep - p.recent;  // m < rivals
+    for (int i = tid; i < p.recent; i += kSelect) kept[m + i] = rivals + i;
+    if (m == 0) return;
     const int32_t* table = p.block_table + static_cast<long long>(b) * p.table_stride;
-    const auto key = [&](int t) {  // a page that is not there is reported by gather or here
+    const auto read = [&](int t) {
         const int page = table[t >> sh];
         if (page < 0 || page >= p.pages) {
             raise_error(p.err, MOE_ERR_BAD_INDEX);
@@ -68,125 +66,177 @@ __global__ void __launch_bounds__(kSelect) select_kernel(const Evict p) {
         }
         return key_of(p.weights[((static_cast<long long>(page) * p.Hkv + hk) << sh) + (t & ((1 << sh) - 1))]);
     };
-    const int rivals = len - p.recent, m = p.keep - p.recent;  // m < rivals
-    uint32_t last = 0;  // the m-th largest key; `left` of those that have it are kept
-    int left = 0;
-    if (m > 0) {
-        left = m;
-        uint32_t mask = 0;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (tid < 256) s_hist[tid] = 0;
-            __syncthreads();
-            for (int t = tid; t < rivals; t += kSelect) {
-                const uint32_t k = key(t);
-                if ((k & mask) == last) atomicAdd(&s_hist[k >> shift & 255], 1);
+    const auto key = [&](int t) { return HELD ? s_key[t] : read(t); };
+    for (int i = tid; i < kBins; i += kSelect) s_bins[i] = 0;
+    if constexpr (HELD) {
+#pragma unroll 4
+        for (int t = tid; t < rivals; t += kSelect) s_key[t] = read(t);
+    }
+    __syncthreads();
+    uint32_t last = 0, mask = 0;  // the m-th largest key; `left` of those that have it are kept
+    int left = m;
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
+        for (int t0 = warp * 32; t0 < rivals; t0 += kSelect) {
+            const int t = t0 + lane;
+            const uint32_t k = t < rivals ? key(t) : 0u;
+            const bool in = t < rivals && (k & mask) == last;
+            const int digit = in ? static_cast<int>((k >> shift) & (bins - 1)) : -1;
+            // equal digits all over the warp (weights that are all alike) are added at once
+            int alike;
+            __match_all_sync(~0u, digit, &alike);
+            if (alike) {
+                if (lane == 0 && digit >= 0) atomicAdd(&s_bins[digit], 32);
+            } else if (in) {
+                atomicAdd(&s_bins[digit], 1);
             }
-            __syncthreads();
-            if (tid == 0) {
-                int d = 255, n = left;
-                for (; d > 0 && s_hist[d] < n; --d) n -= s_hist[d];
-                s_digit = d;
-                s_left = n;
-            }
-            __syncthreads();
-            last |= s_digit << shift;
-            left = s_left;
-            mask |= 255u << shift;
         }
+        __syncthreads();
+        // the bin with the left-th largest: thread i has bins 2 i, 2 i + 1, counted from above
+        const int i = bins / 2 - 1 - tid;
+        const int hi = i >= 0 ? s_bins[2 * i + 1] : 0, lo = i >= 0 ? s_bins[2 * i] : 0;
+        int above = hi + lo;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(~0u, above, o);
+            if (lane >= o) above += y;
+        }
+        if (lane == 31) s_warp[warp] = above;
+        __syncthreads();
+        int before = 0;
+#pragma unroll
+        for (int w = 0; w < kSelect / 32; ++w) before += w < warp ? s_warp[w] : 0;
+        before += above - hi - lo;  // in bins above this thread's
+        if (before < left && left <= before + hi + lo) {
+            s_digit = 2 * i + (left <= before + hi);
+            s_left = left <= before + hi ? left - before : left - before - hi;
+        }
+        if (i >= 0) s_bins[2 * i] = s_bins[2 * i + 1] = 0;
+        __syncthreads();
+        last |= static_cast<uint32_t>(s_digit) << shift;
+        left = s_left;
+        mask |= static_cast<uint32_t>(bins - 1) << shift;
     }
-    int at = 0, same = 0;  // tokens kept, and tokens at the last weight, so far
-    for (int t0 = 0; t0 < rivals && m > 0; t0 += kSelect) {
-        const int t = t0 + tid;
-        const uint32_t k = t < rivals ? key(t) : 0u;
-        const bool tie = t < rivals && k == last;
-        int ties, n;
-        const int tie_at = same + count_before(tie, s_warp, ties);
-        const bool mine = (t < rivals && k > last) || (tie && tie_at < left);
-        const int i = at + count_before(mine, s_warp, n);
-        if (mine && i < p.keep) kept[i] = t;
-        same += ties;
-        at += n;
+    const int run = ((rivals + kSelect - 1) / kSelect) * 32;  // of a warp
+    const int begin = min(rivals, warp * run), end = min(rivals, begin + run);
+    Count c{0, 0};
+    for (int t0 = begin; t0 < end; t0 += 32) {
+        const uint32_t k = t0 + lane < end ? key(t0 + lane) : 0u;
+        const bool in = t0 + lane < end;
+        c.more += __popc(__ballot_sync(~0u, in && k > last));
+        c.same += __popc(__ballot_sync(~0u, in && k == last));
     }
-    for (int i = tid; i < p.recent; i += kSelect) kept[m + i] = rivals + i;
+    if (lane == 0) s_count[warp] = c;
+    __syncthreads();
+    c = Count{0, 0};
+#pragma unroll
+    for (int w = 0; w < kSelect / 32; ++w) {
+        c.more += w < warp ? s_count[w].more : 0;
+        c.same += w < warp ? s_count[w].same : 0;
+    }
+    const unsigned below = (1u << lane) - 1;
+    for (int t0 = begin; t0 < end; t0 += 32) {
+        const bool in = t0 + lane < end;
+        const uint32_t k = in ? key(t0 + lane) : 0u;
+        const unsigned more = __ballot_sync(~0u, in && k > last), same = __ballot_sync(~0u, in && k == last);
+        const int ties = c.same + __popc(same & below);
+        if (in && (k > last || (k == last && ties < left)))
+            kept[c.more + __popc(more & below) + min(ties, left)] = t0 + lane;
+        c.more += __popc(more);
+        c.same += __popc(same);
+    }
 }
 
 template <bool E8>
-__global__ void __launch_bounds__(kGather) gather_kernel(const Evict p, int new_pages) {
-    __shared__ int s_row[256];     // rows of the cache that the new rows come from
+__global__ void __launch_bounds__(kGather)
+gather_kernel(const Evict p, int new_pages, int lane_shift) {
+    __shared__ int s_row[256];       // rows of the cache that the new rows come from
     __shared__ float s_old[2][256];  // E8: their scales (keys, values)
     __shared__ float s_top[2][kGather / 32];
     pdl_wait();
     pdl_trigger();
-    if (__syncthreads_or(stopped(p.err))) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long item = blockIdx.x;
-    const int j = static_cast<int>(item % new_pages);
-    item /= new_pages;
-    const int hk = static_cast<int>(item % p.Hkv), b = static_cast<int>(item / p.Hkv);
-    const int len = p.lens[b], sh = p.page_shift;
-    if (len < 0 || len > p.max_kv) return;  // reported by select_kernel
+    const int j = static_cast<int>(blockIdx.x % new_pages), unit = static_cast<int>(blockIdx.x / new_pages);
+    const int hk = unit % p.Hkv, b = unit / p.Hkv, sh = p.page_shift;
+    // what does not depend on another load comes first
+    const int len = p.lens[b];
+    const int goal = p.new_table[static_cast<long long>(b) * p.new_stride + j];
+    const int place = (j << sh) + tid;  // in the new sequence
+    int t = -1;
+    if (tid < 1 << sh && place < p.keep) t = p.kept[static_cast<long long>(unit) * p.keep + place];
+    if (__syncthreads_or(stopped(p.err)) || len < 0 || len > p.max_kv) return;  // reported by select_kernel
     const int n = min(len, p.keep);
     // (new_lens may be the lengths themselves: whichever of the two is read, n is the same)
     if (j == 0 && hk == 0 && tid == 0) p.new_lens[b] = n;
     const int rows = min(1 << sh, n - (j << sh));
     if (rows <= 0) return;
-    const int goal = p.new_table[static_cast<long long>(b) * p.new_stride + j];
     bool bad = goal < 0 || goal >= p.pages;
-    float kt = 0.f, vt = 0.f;
+    int page = 0;
     if (tid < rows) {
-        const int t = p.kept[(static_cast<long long>(b) * p.Hkv + hk) * p.keep + (j << sh) + tid];
-        const int page = t < 0 || t >= len ? -1
-                                           : p.block_table[static_cast<long long>(b) * p.table_stride + (t >> sh)];
+        page = t < 0 || t >= p.max_kv ? -1 : p.block_table[static_cast<long long>(b) * p.table_stride + (t >> sh)];
         bad |= page < 0 || page >= p.pages;
-        if (!bad) {
-            s_row[tid] = ((page * p.Hkv + hk) << sh) + (t & ((1 << sh) - 1));
-            if constexpr (E8) {
-                const long long at = static_cast<long long>(page) * p.Hkv + hk;
-                kt = s_old[0][tid] = p.k_scale[at];
-                vt = s_old[1][tid] = p.v_scale[at];
-            }
-        }
-    }
-    if constexpr (E8) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            kt = fmaxf(kt, __shfl_xor_sync(~0u, kt, o));
-            vt = fmaxf(vt, __shfl_xor_sync(~0u, vt, o));
-        }
-        if (lane == 0) s_top[0][warp] = kt, s_top[1][warp] = vt;
+        s_row[tid] = bad ? 0 : ((page * p.Hkv + hk) << sh) + (t & ((1 << sh) - 1));
     }
     if (__syncthreads_or(bad)) {
         if (tid == 0) raise_error(p.err, MOE_ERR_BAD_INDEX);
         return;
     }
+    // a row's pieces of 16 bytes on 1 << lane_shift lanes, two rows' loads in flight
+    const int chunks = p.D * (E8 ? 1 : 2) / 16;
+    const int c = tid & ((1 << lane_shift) - 1), step = kGather >> lane_shift;
+    uint4 v[2][2];
+    const auto load = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int i = i0 + u * step;
+            if (i < rows && c < chunks) {
+                const long long at = static_cast<long long>(s_row[i]) * chunks + c;
+                v[u][0] = reinterpret_cast<const uint4*>(p.k_pages)[at];
+                v[u][1] = reinterpret_cast<const uint4*>(p.v_pages)[at];
+            }
+        }
+    };
+    load(tid >> lane_shift);
+    const float weight = tid < rows ? p.weights[s_row[tid]] : 0.f;
     const int goal_row = (goal * p.Hkv + hk) << sh;
     float top[2] = {0.f, 0.f};
     if constexpr (E8) {
-#pragma unroll
-        for (int w = 0; w < kGather / 32; ++w) {
-            top[0] = fmaxf(top[0], s_top[0][w]);
-            top[1] = fmaxf(top[1], s_top[1][w]);
+        if (tid < rows) {
+            const long long at = static_cast<long long>(page) * p.Hkv + hk;
+            top[0] = s_old[0][tid] = p.k_scale[at];
+            top[1] = s_old[1][tid] = p.v_scale[at];
         }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top[x] = fmaxf(top[x], __shfl_xor_sync(~0u, top[x], o));
+            if (lane == 0) s_top[x][warp] = top[x];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int w = 0; w < kGather / 32; ++w) top[x] = fmaxf(top[x], s_top[x][w]);
         if (tid < 2) (tid == 0 ? p.k_scale : p.v_scale)[static_cast<long long>(goal) * p.Hkv + hk] = top[tid];
     }
-    if (tid < rows) p.weights[goal_row + tid] = p.weights[s_row[tid]];
-    const int bytes = p.D * (E8 ? 1 : 2), chunks = bytes / 16;
-    for (int x = tid; x < 2 * rows * chunks; x += kGather) {
-        const int which = x >= rows * chunks, y = which ? x - rows * chunks : x;
-        const int i = y / chunks, c = y % chunks;
-        uint8_t* pages = which ? p.v_pages : p.k_pages;
-        uint4 v = reinterpret_cast<const uint4*>(pages + static_cast<long long>(s_row[i]) * bytes)[c];
-        if constexpr (E8) {
-            const float old = s_old[which][i];
-            if (old != top[which]) {
-                const float f = old / top[which];
-                v.x = rescale_e4m3x4(v.x, f);
-                v.y = rescale_e4m3x4(v.y, f);
-                v.z = rescale_e4m3x4(v.z, f);
-                v.w = rescale_e4m3x4(v.w, f);
+    if (tid < rows) p.weights[goal_row + tid] = weight;
+    for (int i0 = tid >> lane_shift; i0 < rows; i0 += 2 * step) {
+        if (i0 >= 2 * step) load(i0);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int i = i0 + u * step;
+            if (i >= rows || c >= chunks) continue;
+            if constexpr (E8) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float old = s_old[x][i];
+                    if (old != top[x]) v[u][x] = rescale_e4m3x16(v[u][x], old / top[x]);
+                }
             }
+            const long long at = static_cast<long long>(goal_row + i) * chunks + c;
+            reinterpret_cast<uint4*>(p.k_pages)[at] = v[u][0];
+            reinterpret_cast<uint4*>(p.v_pages)[at] = v[u][1];
         }
-        reinterpret_cast<uint4*>(pages + static_cast<long long>(goal_row + i) * bytes)[c] = v;
     }
 }
 
@@ -199,14 +249,20 @@ cudaError_t launch_evict(const Evict& p, cudaStream_t st) {
     const long long items = static_cast<long long>(p.B) * p.Hkv * new_pages;
     if (items > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     {
+        const bool held = p.max_kv <= kHeld;
+        const int smem = held ? 4 * p.max_kv : 0;
+        auto kfn = held ? select_kernel<true> : select_kernel<false>;
+        cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kHeld);
+        if (e != cudaSuccess) return e;
         LaunchScope ls("kv_select", st);
-        const cudaError_t e = launch_pdl(select_kernel, dim3(static_cast<unsigned>(p.B * p.Hkv)),
-                                         dim3(kSelect), 0, st, p);
+        e = launch_pdl(kfn, dim3(static_cast<unsigned>(p.B * p.Hkv)), dim3(kSelect), smem, st, p);
         if (e != cudaSuccess) return e;
     }
+    int lane_shift = 0;
+    while ((16 << lane_shift) < p.D * (p.k_scale != nullptr ? 1 : 2)) ++lane_shift;
     LaunchScope ls("kv_gather", st);
     return launch_pdl(p.k_scale != nullptr ? gather_kernel<true> : gather_kernel<false>,
-                      dim3(static_cast<unsigned>(items)), dim3(kGather), 0, st, p, new_pages);
+                      dim3(static_cast<unsigned>(items)), dim3(kGather), 0, st, p, new_pages, lane_shift);
 }
 
 }  // namespace attn
