@@ -13,6 +13,7 @@ namespace attn {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kAhead = 4;  // rows of a lane whose loads are in flight at once
 
 // The page tasks of sequence b are numbered from here: the pages that n rows touch are no
 // more than floor((r + n) / P) - floor(r / P) + 2 for any r.
@@ -43,7 +44,7 @@ __device__ __forceinline__ float scale_for(float a) {
 }
 
 template <int LPR, int SWAP>
-__global__ void __launch_bounds__(kWarps * 32) append8_kernel(const Append8 p) {
+__global__ void __launch_bounds__(kWarps * 32, 3) append8_kernel(const Append8 p) {
     constexpr int RPW = 32 / LPR;
     extern __shared__ __align__(16) float s_x[];  // [rows of the page][LPR * 8]
     __shared__ __align__(16) bf16 s_buf[SWAP == SWAP_ROW ? kWarps * RPW * 128 : 8];
@@ -56,6 +57,25 @@ __global__ void __launch_bounds__(kWarps * 32) append8_kernel(const Append8 p) {
     const int D = r.a.D, Hkv = r.a.Hkv, sh = r.page_shift;
     const bool value = blockIdx.y >= Hkv;
     const int hk = static_cast<int>(blockIdx.y) - (value ? Hkv : 0);
+    // what needs no other load comes first
+    const bool live = piece * 8 < D;
+    const bool norm = !value && r.wq != nullptr;
+    float w[8], wp[8];  // the norm weights of this lane's values and of their partners
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = wp[e] = 1.f;
+    if (norm && live) {
+        load_weights(r.wk, piece, w);
+        if constexpr (SWAP == SWAP_OWN) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) wp[e] = w[e ^ 1];
+        } else if constexpr (SWAP == SWAP_LANE) {
+            const int hop = r.rot >> 4;
+            load_weights(r.wk, piece < hop ? piece + hop : piece < 2 * hop ? piece - hop : piece, wp);
+        } else if constexpr (SWAP == SWAP_ROW) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) wp[e] = __ldg(r.wk + partner_of(piece * 8 + e, r.rot, r.interleaved));
+        }
+    }
     if (__syncthreads_or(stopped(r.err))) return;
     if (blockIdx.x == 0 && blockIdx.y == 0)  // every sequence's offsets, whatever tasks they get
         for (int b = threadIdx.x; b < p.B; b += kWarps * 32) {
@@ -77,66 +97,71 @@ __global__ void __launch_bounds__(kWarps * 32) append8_kernel(const Append8 p) {
     const int o = lo & ((1 << sh) - 1);
     const int row0 = q0 + lo - before;
     const int page = p.block_table[static_cast<long long>(b) * p.table_stride + pg];
+    const Heads src = value ? r.v : r.k;
+    uint4 in[kAhead];
+    int pos[kAhead];
+    const auto load = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = i0 + u * kWarps * RPW + sub;
+            in[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (i < rows && live) in[u] = *reinterpret_cast<const uint4*>(src.row(row0 + i, hk) + piece * 8);
+            pos[u] = SWAP != SWAP_NONE && !value && i < rows ? r.positions[row0 + i] : 0;
+        }
+    };
+    load(warp * RPW);
     if (page < 0 || page >= r.pages) {
         if (threadIdx.x == 0) raise_error(r.err, MOE_ERR_BAD_INDEX);
         return;
     }
     float* scale_at = (value ? p.v_scale : p.k_scale) + static_cast<long long>(page) * Hkv + hk;
     const float old = o > 0 ? *scale_at : 0.f;
-    const bool live = piece * 8 < D;
-    const bool norm = !value && r.wq != nullptr;
-    const Heads src = value ? r.v : r.k;
-
-    float w[8], wp[8];  // the norm weights of this lane's values and of their partners
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int i = piece * 8 + e;
-        w[e] = norm && live ? r.wk[i] : 1.f;
-        wp[e] = norm && live && SWAP != SWAP_NONE ? r.wk[partner_of(i, r.rot, r.interleaved)] : 1.f;
-    }
     bf16* buf = s_buf + (SWAP == SWAP_ROW ? (warp * RPW + sub) * 128 : 0);
     float top = 0.f;
-    for (int i0 = warp * RPW; i0 < rows; i0 += kWarps * RPW) {
-        const int i = i0 + sub;
-        const bool mine = i < rows && live;
-        uint4 in = make_uint4(0u, 0u, 0u, 0u);
-        if (mine) in = *reinterpret_cast<const uint4*>(src.row(row0 + i, hk) + piece * 8);
-        float x[8];
-        unpack8(in, x);
-        if (!value) {
-            float rr = 1.f;
-            if (norm) {
-                float s0 = 0.f, s1 = 0.f;
+    const float inv_d = 1.f / static_cast<float>(D);
+    for (int i0 = warp * RPW; i0 < rows; i0 += kAhead * kWarps * RPW) {
+        if (i0 > warp * RPW) load(i0);
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) fma2(s0, s1, x[e], x[e + 1], x[e], x[e + 1]);
-                rr = rsqrtf(row_sum<LPR>(s0 + s1) / static_cast<float>(D) + r.eps);
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = i0 + u * kWarps * RPW + sub;
+            if (i - sub >= rows) break;  // the whole warp
+            float x[8];
+            unpack8(in[u], x);
+            if (!value) {
+                float rr = 1.f;
+                if (norm) {
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) fma2(s0, s1, x[e], x[e + 1], x[e], x[e + 1]);
+                    rr = rsqrtf(row_sum<LPR>(s0 + s1) * inv_d + r.eps);
+                }
+                float a[8], c[8], y[8];
+                bool bad = false;
+                if constexpr (SWAP != SWAP_NONE) {
+                    bad = pos[u] < 0 || pos[u] >= r.table_rows;
+                    if (bad && piece == 0) raise_error(r.err, MOE_ERR_BAD_INDEX);
+                    load_rotation<SWAP>(r.table + static_cast<long long>(bad ? 0 : pos[u]) * (r.rot >> 1), r.rot,
+                                        r.interleaved, piece, a, c);
+                    float other[8];
+                    partners<LPR, SWAP>(in[u], x, r.rot, r.interleaved, piece, buf, other);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        y[e] = (x[e] * (w[e] * a[e]) + other[e] * (wp[e] * c[e])) * rr;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = x[e] * w[e] * rr;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = bad ? 0.f : y[e];  // a refused row has no say in the scale
             }
-            float a[8], c[8], y[8];
-            bool bad = false;
-            if constexpr (SWAP != SWAP_NONE) {
-                const int pos = i < rows ? r.positions[row0 + i] : 0;
-                bad = pos < 0 || pos >= r.table_rows;
-                if (bad && piece == 0) raise_error(r.err, MOE_ERR_BAD_INDEX);
-                load_rotation<SWAP>(r.table + static_cast<long long>(bad ? 0 : pos) * (r.rot >> 1), r.rot,
-                                    r.interleaved, piece, a, c);
-                float other[8];
-                partners<LPR, SWAP>(in, x, r.rot, r.interleaved, piece, buf, other);
+            if (i < rows && live) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = (x[e] * (w[e] * a[e]) + other[e] * (wp[e] * c[e])) * rr;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = x[e] * w[e] * rr;
+                for (int e = 0; e < 8; ++e)
+                    if (fabsf(x[e]) <= 3.402823466e+38f) top = fmaxf(top, fabsf(x[e]));
+                float4* dst = reinterpret_cast<float4*>(s_x + i * (LPR * 8) + piece * 8);
+                dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+                dst[1] = make_float4(x[4], x[5], x[6], x[7]);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = bad ? 0.f : y[e];  // a refused row has no say in the scale
-        }
-        if (mine) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (fabsf(x[e]) <= 3.402823466e+38f) top = fmaxf(top, fabsf(x[e]));
-            float4* dst = reinterpret_cast<float4*>(s_x + i * (LPR * 8) + piece * 8);
-            dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-            dst[1] = make_float4(x[4], x[5], x[6], x[7]);
         }
     }
 #pragma unroll

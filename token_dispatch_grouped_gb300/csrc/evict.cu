@@ -28,7 +28,7 @@ __device__ __forceinline__ uint32_t key_of(float w) {
 constexpr int kBins = 2048;
 constexpr int kHeld = 48 * 1024;  // weights in shared memory at most: 192 KB
 
-// How many of a warp's keys are above `last`, or at it; from `t` to `end` in steps of 32.
+// How many of a warp's keys are above the last one kept, and at it.
 struct Count {
     int more, same;
 };
@@ -36,7 +36,7 @@ struct Count {
 // HELD: keys in shared memory.
 template <bool HELD>
 __global__ void __launch_bounds__(kSelect, 2) select_kernel(const Evict p) {
-    extern __shared__ uint32_t s_key[];
+    extern __shared__ __align__(16) uint32_t s_key[];
     __shared__ int s_bins[kBins];
     __shared__ int s_warp[kSelect / 32];
     __shared__ Count s_count[kSelect / 32];
@@ -58,37 +58,52 @@ __global__ void __launch_bounds__(kSelect, 2) select_kernel(const Evict p) {
     for (int i = tid; i < p.recent; i += kSelect) kept[m + i] = rivals + i;
     if (m == 0) return;
     const int32_t* table = p.block_table + static_cast<long long>(b) * p.table_stride;
+    // four tokens at a time, which share a page; past the rivals: 0, and not counted
     const auto read = [&](int t) {
         const int page = table[t >> sh];
         if (page < 0 || page >= p.pages) {
             raise_error(p.err, MOE_ERR_BAD_INDEX);
-            return 0u;
+            return make_uint4(0u, 0u, 0u, 0u);
         }
-        return key_of(p.weights[((static_cast<long long>(page) * p.Hkv + hk) << sh) + (t & ((1 << sh) - 1))]);
+        const float4 w = *reinterpret_cast<const float4*>(
+            p.weights + ((static_cast<long long>(page) * p.Hkv + hk) << sh) + (t & ((1 << sh) - 1)));
+        return make_uint4(key_of(w.x), key_of(w.y), key_of(w.z), key_of(w.w));
     };
-    const auto key = [&](int t) { return HELD ? s_key[t] : read(t); };
+    const auto keys = [&](int t, uint32_t (&k)[4]) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (t < rivals) v = HELD ? *reinterpret_cast<const uint4*>(s_key + t) : read(t);
+        k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+    };
     for (int i = tid; i < kBins; i += kSelect) s_bins[i] = 0;
     if constexpr (HELD) {
-#pragma unroll 4
-        for (int t = tid; t < rivals; t += kSelect) s_key[t] = read(t);
+#pragma unroll 8
+        for (int t = 4 * tid; t < rivals; t += 4 * kSelect) *reinterpret_cast<uint4*>(s_key + t) = read(t);
     }
     __syncthreads();
     uint32_t last = 0, mask = 0;  // the m-th largest key; `left` of those that have it are kept
     int left = m;
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
-        for (int t0 = warp * 32; t0 < rivals; t0 += kSelect) {
-            const int t = t0 + lane;
-            const uint32_t k = t < rivals ? key(t) : 0u;
-            const bool in = t < rivals && (k & mask) == last;
-            const int digit = in ? static_cast<int>((k >> shift) & (bins - 1)) : -1;
+        for (int t0 = warp * 128; t0 < rivals; t0 += 4 * kSelect) {
+            const int t = t0 + 4 * lane;
+            uint32_t k[4];
+            keys(t, k);
+            int digit[4];
+            bool same = true;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool in = t + e < rivals && (k[e] & mask) == last;
+                digit[e] = in ? static_cast<int>((k[e] >> shift) & (bins - 1)) : -1;
+                same &= digit[e] == digit[0];
+            }
             // equal digits all over the warp (weights that are all alike) are added at once
-            int alike;
-            __match_all_sync(~0u, digit, &alike);
-            if (alike) {
-                if (lane == 0 && digit >= 0) atomicAdd(&s_bins[digit], 32);
-            } else if (in) {
-                atomicAdd(&s_bins[digit], 1);
+            const int first = __shfl_sync(~0u, digit[0], 0);
+            if (__all_sync(~0u, same && digit[0] == first)) {
+                if (lane == 0 && first >= 0) atomicAdd(&s_bins[first], 128);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (digit[e] >= 0) atomicAdd(&s_bins[digit[e]], 1);
             }
         }
         __syncthreads();
@@ -117,33 +132,60 @@ __global__ void __launch_bounds__(kSelect, 2) select_kernel(const Evict p) {
         left = s_left;
         mask |= static_cast<uint32_t>(bins - 1) << shift;
     }
-    const int run = ((rivals + kSelect - 1) / kSelect) * 32;  // of a warp
+    const int run = (rivals + 4 * kSelect - 1) / (4 * kSelect) * 128;  // tokens of a warp
     const int begin = min(rivals, warp * run), end = min(rivals, begin + run);
-    Count c{0, 0};
-    for (int t0 = begin; t0 < end; t0 += 32) {
-        const uint32_t k = t0 + lane < end ? key(t0 + lane) : 0u;
-        const bool in = t0 + lane < end;
-        c.more += __popc(__ballot_sync(~0u, in && k > last));
-        c.same += __popc(__ballot_sync(~0u, in && k == last));
+    // of four tokens: how many are above `last`, and, in the upper half, how many are at it
+    const auto count = [&](int t, const uint32_t (&k)[4]) {
+        int n = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (t + e < rivals) n += k[e] > last ? 1 : k[e] == last ? 1 << 16 : 0;
+        return n;
+    };
+    int more = 0, same = 0;
+    for (int t0 = begin; t0 < end; t0 += 128) {
+        uint32_t k[4];
+        keys(t0 + 4 * lane, k);
+        const int n = count(t0 + 4 * lane, k);
+        more += n & 0xffff;
+        same += n >> 16;
     }
-    if (lane == 0) s_count[warp] = c;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        more += __shfl_xor_sync(~0u, more, o);
+        same += __shfl_xor_sync(~0u, same, o);
+    }
+    if (lane == 0) s_count[warp] = Count{more, same};
     __syncthreads();
-    c = Count{0, 0};
+    more = same = 0;
 #pragma unroll
     for (int w = 0; w < kSelect / 32; ++w) {
-        c.more += w < warp ? s_count[w].more : 0;
-        c.same += w < warp ? s_count[w].same : 0;
+        more += w < warp ? s_count[w].more : 0;
+        same += w < warp ? s_count[w].same : 0;
     }
-    const unsigned below = (1u << lane) - 1;
-    for (int t0 = begin; t0 < end; t0 += 32) {
-        const bool in = t0 + lane < end;
-        const uint32_t k = in ? key(t0 + lane) : 0u;
-        const unsigned more = __ballot_sync(~0u, in && k > last), same = __ballot_sync(~0u, in && k == last);
-        const int ties = c.same + __popc(same & below);
-        if (in && (k > last || (k == last && ties < left)))
-            kept[c.more + __popc(more & below) + min(ties, left)] = t0 + lane;
-        c.more += __popc(more);
-        c.same += __popc(same);
+    for (int t0 = begin; t0 < end; t0 += 128) {
+        const int t = t0 + 4 * lane;
+        uint32_t k[4];
+        keys(t, k);
+        const int n = count(t, k);
+        int upto = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(~0u, upto, o);
+            if (lane >= o) upto += y;
+        }
+        int above = more + ((upto - n) & 0xffff), ties = same + ((upto - n) >> 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (t + e >= rivals) break;
+            const int at = above + min(ties, left);
+            if (k[e] > last || (k[e] == last && ties < left)) kept[at] = t + e;
+            above += k[e] > last;
+            ties += k[e] == last;
+        }
+        const int all = __shfl_sync(~0u, upto, 31);
+        more += all & 0xffff;
+        same += all >> 16;
     }
 }
 
@@ -250,9 +292,9 @@ cudaError_t launch_evict(const Evict& p, cudaStream_t st) {
     if (items > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     {
         const bool held = p.max_kv <= kHeld;
-        const int smem = held ? 4 * p.max_kv : 0;
+        const int smem = held ? 4 * p.max_kv + 16 : 0;
         auto kfn = held ? select_kernel<true> : select_kernel<false>;
-        cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kHeld);
+        cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kHeld + 16);
         if (e != cudaSuccess) return e;
         LaunchScope ls("kv_select", st);
         e = launch_pdl(kfn, dim3(static_cast<unsigned>(p.B * p.Hkv)), dim3(kSelect), smem, st, p);
