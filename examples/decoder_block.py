@@ -7,7 +7,8 @@ A block is x1 = x + attention(x), x2 = x1 + moe(x1). The projections are plain m
 products; everything between them runs in the library: norm and rotary positions of the
 heads, attention over the packed sequences (and its backward), and the MoE layer. Serving
 appends each new token's keys and values to pages, attends over them and runs the layer on
-the result; its outputs are compared with the packed forward's.
+the result; its outputs are compared with the packed forward's. Then the same sequences are
+served from a smaller cache: e4m3 pages, cut to the tokens that get the most attention.
 """
 import os
 import sys
@@ -96,6 +97,65 @@ class Block:
         return x1 + y, x1, r.ids
 
 
+class SmallCache:
+    """Pages of 8 bits for `seqs` sequences of up to `most` tokens and, beside them, pages for
+    `keep` of their tokens and `new` more."""
+
+    def __init__(self, b, seqs, most, keep, new, page=64):
+        wide, less = -(-most // page), -(-(keep + new) // page)
+        order = torch.randperm(seqs * (wide + less), device="cuda").to(torch.int32)
+        self.table = order[:seqs * wide].view(seqs, wide)
+        self.less = order[seqs * wide:].view(seqs, less)
+        self.keep, self.b = keep, b
+        pages = torch.zeros(order.numel(), b.Hkv, page, b.D, device="cuda")
+        self.k, self.v = (pages.to(torch.float8_e4m3fn) for _ in range(2))
+        self.ks, self.vs = (torch.zeros(order.numel(), b.Hkv, device="cuda") for _ in range(2))
+        self.weights = torch.zeros(order.numel(), b.Hkv, page, device="cuda")
+
+    def attend(self, x, positions, cu, lens, window, fresh):
+        """Appends the new tokens x of every sequence, the last `window` of each attend."""
+        b, att = self.b, self.b.att
+        _, q, k, v = b.heads(x)
+        q = att.append8(q, k, v, b.wq, b.wk, positions, cu, self.table, lens, self.k, self.v,
+                        self.ks, self.vs)
+        rows = (cu[1:, None] - window + torch.arange(window, device="cuda")).flatten().long()
+        o = att.decode8(q[rows], self.k, self.v, self.ks, self.vs, self.table, lens,
+                        self.table.shape[1] * self.k.shape[2], weights=self.weights, fresh=fresh)
+        return x[rows] + o.view(rows.numel(), -1) @ b.Wo.T
+
+    def cut(self, lens, recent):
+        """Keeps `keep` tokens of each sequence, the newest `recent` among them; the pages of
+        the whole ones are free then."""
+        size = self.table.shape[1] * self.k.shape[2]
+        _, kept = self.b.att.evict(self.k, self.v, self.weights, self.table, lens, size, self.keep,
+                                   recent, self.less, k_scales=self.ks, v_scales=self.vs,
+                                   new_lens=lens)
+        self.table = self.less
+        return kept
+
+
+def serve_small(b, x, lens, cu, pos, new, keep, recent):
+    """x1 of the last `new` tokens of every sequence from a small cache: the prompts enter it,
+    their last 16 tokens vote, each is cut, and the other tokens follow one by one."""
+    n, dev = len(lens), x.device
+    prompt = torch.tensor(lens, device=dev) - new
+    rows = torch.cat([torch.arange(int(cu[i]), int(cu[i]) + int(p)) for i, p in enumerate(prompt)])
+    rows = rows.to(dev)
+    cu_p = torch.cat([prompt[:1] * 0, prompt.cumsum(0)]).to(torch.int32)
+    cache = SmallCache(b, n, max(lens), keep, new)
+    held = prompt.to(torch.int32)
+    cache.attend(x[rows], pos[rows], cu_p, held, 16, True)
+    cache.cut(held, recent)
+    one = torch.arange(n + 1, dtype=torch.int32, device=dev)
+    out = []
+    for i in range(new):
+        at = cu[:-1].long() + prompt + i
+        held += 1
+        out.append(cache.attend(x[at], pos[at], one, held, 1, False))
+    b.att.check_error()
+    return torch.stack(out, 1), held
+
+
 def main():
     b = Block()
     lens = [300, 37, 512]
@@ -154,6 +214,12 @@ def main():
     print(f"served {new} tokens of {n} sequences through the block: relative difference to the "
           f"packed forward {worst:.1e}, the same experts for {same} of {new * n}")
     assert worst < 1e-2 and same >= 0.8 * new * n
+
+    got, held = serve_small(b, x, lens, cu, pos, new, keep=192, recent=32)
+    want = torch.stack([x1[cu[1:].long() - new + i] for i in range(new)], 1)
+    print(f"served them from e4m3 pages cut to {held.tolist()} tokens: relative difference "
+          f"{off(got, want):.1e}")
+    assert bool(torch.isfinite(got.float()).all())
     return worst
 
 

@@ -373,3 +373,63 @@ def test_a_value_that_is_not_finite_stays_in_its_sequence():
     assert torch.equal(got[[0, 2]], want[[0, 2]]) and got[1].isnan().all()
     others = [p for p in range(w.shape[0]) if p not in table.cpu().numpy()[1, :-(-150 // 16)]]
     assert torch.equal(a[others], b[others])
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("seqs", [3, 400])
+def test_no_cached_token_at_all(seqs, bits):
+    """A stated bound of 0: zeros, weights untouched, and no workspace to write to."""
+    from token_dispatch_grouped_gb300.attention import Attention
+    att, table = Attention(4, 2, 64), torch.zeros(seqs, 1, dtype=torch.int32, device="cuda")
+    k, _, s, _ = cache8(2, 2, 16, 64)
+    pages = (k, k, s, s) if bits == 8 else (k.bfloat16(), k.bfloat16())
+    w = torch.rand(2, 2, 16, device="cuda")
+    before, q = w.clone(), rnd((seqs, 4, 64), 1).cuda()
+    out = decode_of(att, pages, q, table, ints([0] * seqs), 0, weights=w,
+                    out=torch.full_like(q, 3))
+    assert bool((out == 0).all()) and torch.equal(w, before)
+
+
+MANY = [  # sequences, longest, n, Hq, Hkv, D, page: parts for more CTAs than the GPU holds
+    (64, 900, 1, 8, 8, 64, 64), (40, 1500, 3, 8, 2, 128, 16), (300, 300, 1, 16, 2, 96, 8),
+    (1100, 200, 1, 2, 1, 64, 64)]
+
+
+@pytest.mark.parametrize("case", MANY)
+def test_decode8_many_parts(case):
+    """Uneven sequences, empty ones among them, whose parts the CTAs take in turn; then one of
+    them with a length out of range: the others keep every bit, in a replayed graph too."""
+    seqs, longest, n, Hq, Hkv, D, P = case
+    from token_dispatch_grouped_gb300 import binding as B
+    from token_dispatch_grouped_gb300.attention import Attention
+    r = np.random.default_rng(seqs)
+    lens = [int(x) for x in r.integers(0, longest, seqs)]
+    lens[3], lens[5], lens[-1] = 0, longest, 1
+    att, full = Attention(Hq, Hkv, D), (lens, n, Hq, Hkv, D, P)
+    q, pages, kv, table, kv_lens, w = decode_data(full, 8)
+    got = w.clone()
+    out = decode_of(att, pages, q, table, kv_lens, longest, weights=got)
+    assert torch.equal(out, decode_of(att, pages, q, table, kv_lens, longest))
+    ref, bound, add = reference(full, q, kv, att.scale)
+    within(out, ref, bound, "many parts")
+    for b in (0, 5, seqs // 2, seqs - 1):
+        t = np.arange(lens[b])
+        page, off = table.cpu().numpy()[b, t // P], t % P
+        had = np.where(t >= lens[b] - n, 0.0, f64(w)[page, :, off].T)
+        want = (had + add[b]).T
+        assert (np.abs(f64(got)[page, :, off] - want) <= (O.F * add[b] + 2.0 ** -22 * want.T).T).all()
+    args = (q, table, kv_lens, longest)
+    decode_of(att, pages, *args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = decode_of(att, pages, *args)
+    for _ in range(3):
+        again.zero_()
+        graph.replay()
+        assert torch.equal(again, out)
+    kv_lens[5] = longest + 1
+    graph.replay()
+    assert B.moe_get_error() == B.MOE_ERR_BAD_INDEX
+    rows = torch.arange(seqs * n, device="cuda") // n != 5
+    assert torch.equal(again[rows], out[rows])

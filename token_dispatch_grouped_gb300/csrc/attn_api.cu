@@ -206,7 +206,7 @@ int decode_of(const moe_attn_shape& a, int32_t B, int32_t n, int32_t max_kv, flo
     p.block_table = block_table;
     p.table_stride = table_stride;
     p.kv_lens = kv_lens;
-    p.weights = weights;
+    p.weights = max_kv > 0 ? weights : nullptr;  // no token, no workspace
     p.fresh = fresh;
     p.ws = static_cast<float*>(ws);
     p.err = err;

@@ -522,7 +522,7 @@ DecodeSpace decode_space(const Decode& d, const DecodePlan& pl) {
     s.lse = weights ? up(rows) : 0;
     s.scores = weights ? rows * s.pitch : 0;
     s.total = s.part + s.lse + s.scores;
-    if (d.k_scale != nullptr && decode_numbered(d.a, d.B, pl)) s.total += 4;  // the count
+    if (d.k_scale != nullptr && decode_numbered(d.a, d.B, d.max_kv, pl)) s.total += 4;  // the count
     return s;
 }
 

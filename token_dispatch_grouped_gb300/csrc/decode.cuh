@@ -36,11 +36,11 @@ struct DecodePlan {
 DecodePlan decode_plan(const moe_attn_shape& a, int B, int n, int max_kv, bool e8);
 
 // Whether decode8.cu's CTAs stay and take numbered parts (with a count of the taken ones in the
-// workspace): where the parts are more than the GPU holds at once and a CTA can number the
-// sequences in shared memory.
+// workspace, which a call without cached tokens has not): where the parts are more than the GPU
+// holds at once and a CTA can number the sequences in shared memory.
 constexpr int kNumberedSeqs = 1024;
-inline bool decode_numbered(const moe_attn_shape& a, int B, const DecodePlan& pl) {
-    return B <= kNumberedSeqs &&
+inline bool decode_numbered(const moe_attn_shape& a, int B, int max_kv, const DecodePlan& pl) {
+    return max_kv > 0 && B <= kNumberedSeqs &&
            static_cast<long long>(B) * a.Hkv * pl.parts * pl.row_tiles > 2 * num_sms();
 }
 

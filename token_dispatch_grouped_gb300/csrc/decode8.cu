@@ -590,7 +590,7 @@ cudaError_t decode8(const Decode& d, cudaStream_t st) {
     if (!make_tmap_e4m3(&mk, d.k_pages, cache_rows, d.a.D, DP, box) ||
         !make_tmap_e4m3(&mv, d.v_pages, cache_rows, d.a.D, DP, box))
         return cudaErrorInvalidValue;
-    int* tickets = decode_numbered(d.a, d.B, pl)
+    int* tickets = decode_numbered(d.a, d.B, d.max_kv, pl)
                        ? reinterpret_cast<int*>(d.ws + decode_space(d, pl).total) - 4
                        : nullptr;
     const int g = d.a.Hq / d.a.Hkv * d.n, rows = g < kRowTile ? g : kRowTile;
