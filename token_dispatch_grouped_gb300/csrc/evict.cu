@@ -58,16 +58,20 @@ __global__ void __launch_bounds__(kSelect, 2) select_kernel(const Evict p) {
     for (int i = tid; i < p.recent; i += kSelect) kept[m + i] = rivals + i;
     if (m == 0) return;
     const int32_t* table = p.block_table + static_cast<long long>(b) * p.table_stride;
-    // four tokens at a time, which share a page; past the rivals: 0, and not counted
-    const auto read = [&](int t) {
-        const int page = table[t >> sh];
-        if (page < 0 || page >= p.pages) {
-            raise_error(p.err, MOE_ERR_BAD_INDEX);
-            return make_uint4(0u, 0u, 0u, 0u);
-        }
+    // four tokens at a time, which share a page; a page that is not there is reported
+    const auto page_of = [&](int t) {
+        const int page = t < rivals ? table[t >> sh] : 0;
+        return page >= 0 && page < p.pages ? page : -1;
+    };
+    const auto at = [&](int page, int t) {
         const float4 w = *reinterpret_cast<const float4*>(
-            p.weights + ((static_cast<long long>(page) * p.Hkv + hk) << sh) + (t & ((1 << sh) - 1)));
+            p.weights + ((static_cast<long long>(max(page, 0)) * p.Hkv + hk) << sh) + (t & ((1 << sh) - 1)));
         return make_uint4(key_of(w.x), key_of(w.y), key_of(w.z), key_of(w.w));
+    };
+    const auto read = [&](int t) {
+        const int page = page_of(t);
+        if (page < 0) raise_error(p.err, MOE_ERR_BAD_INDEX);
+        return at(page, t);
     };
     const auto keys = [&](int t, uint32_t (&k)[4]) {
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -76,8 +80,23 @@ __global__ void __launch_bounds__(kSelect, 2) select_kernel(const Evict p) {
     };
     for (int i = tid; i < kBins; i += kSelect) s_bins[i] = 0;
     if constexpr (HELD) {
-#pragma unroll 8
-        for (int t = 4 * tid; t < rivals; t += 4 * kSelect) *reinterpret_cast<uint4*>(s_key + t) = read(t);
+        bool missing = false;
+        for (int t0 = 4 * tid; t0 < rivals; t0 += 4 * 4 * kSelect) {  // four loads in flight
+            int page[4];
+            uint4 k[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) page[u] = page_of(t0 + u * 4 * kSelect);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                missing |= page[u] < 0;
+                k[u] = at(page[u], t0 + u * 4 * kSelect);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (t0 + u * 4 * kSelect < rivals)
+                    *reinterpret_cast<uint4*>(s_key + t0 + u * 4 * kSelect) = k[u];
+        }
+        if (missing) raise_error(p.err, MOE_ERR_BAD_INDEX);
     }
     __syncthreads();
     uint32_t last = 0, mask = 0;  // the m-th largest key; `left` of those that have it are kept
