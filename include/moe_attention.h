@@ -184,6 +184,7 @@ typedef struct {
  *   e4m3(x / scale), rounded once from fp32 (keys) or bf16 (values). A value that is
  *   not finite is stored as NaN.
  * Pages of two sequences, or twice in one, must not be the same where the call writes.
+ * B <= 65535.
  * Where cu_new does not ascend, nothing holds of what the call stores. */
 int moe_kv8_append(moe_attn_shape a, int32_t B, int32_t T, int32_t max_kv, moe_heads q,
                    moe_heads k, moe_heads v, const float* wq, const float* wk, float eps,
@@ -211,7 +212,9 @@ int moe_attention_decode_weights(moe_attn_shape a, int32_t B, int32_t n, int32_t
                                  moe_heads out, void* ws, size_t ws_bytes, void* stream);
 
 /* moe_attention_decode over the 8-bit cache; weights (NULL: not kept) and fresh as
- * moe_attention_decode_weights. with_weights: whether weights will be given. */
+ * moe_attention_decode_weights. with_weights: whether weights will be given. Keys and
+ * values enter the products as they are (in fp16, where e4m3 is exact), the softmax
+ * weights rounded to fp16. */
 size_t moe_attention_decode8_workspace_size(moe_attn_shape a, int32_t B, int32_t n,
                                             int32_t max_kv, int32_t with_weights);
 int moe_attention_decode8(moe_attn_shape a, int32_t B, int32_t n, int32_t max_kv, float scale,

@@ -4,8 +4,12 @@
 // A CTA takes the rows that a page gets of one head's keys or values: x in fp32 to shared
 // memory with their largest |x|, then p = the smallest power of two with |x| <= 448 p, the
 // page's scale = max(scale, p) (p alone where the page begins), the rows already there moved
-// to it if it grew, and the new ones as e4m3(x / scale). Bound by memory where there are
-// many tokens (2 + 1 bytes a value), by the chain lengths -> table -> rows where there are few.
+// to it if it grew, and the new ones as e4m3(x / scale). The scales are powers of two: e4m3 is a
+// floating format, so they cost no precision, and rows that move are not rounded twice. The page
+// is the CTA's, so no atomics and one launch. By its bytes (3 a value) 4096 tokens of 8 heads of
+// 128 need 4 us; they take 19.4, the chain offsets -> lengths -> rows -> rotation of a page's
+// CTA over two and a half waves of them (22.5 with one row's load in flight a lane). The queries
+// are norm_rope's.
 #include "norm_rope.cuh"
 
 namespace moe {

@@ -387,86 +387,68 @@ __global__ void __launch_bounds__(128) join_kernel(const DecodeParams p) {
 // 4 (G n + 2) bytes a token and head are moved, against the 4 D (2 D for e4m3) that the decode
 // kernel reads for it. A warp takes 128 tokens, four a lane, and the rows that are `split` modulo
 // `splits` of their sequence and head, four rows' loads in flight; the splits are added in their
-// order. (One row's load at a time: 55 us instead of MEASURED for 1.07 million tokens of 8 heads
-// of 4 rows. With the log-sum-exps formed here, so that the join could run beside it, 100 us.)
+// order. (3 x 16 new tokens over up to 5000, 80 rows a head: 24 us with a thread for all rows, 11
+// so. 64 sequences of up to 32768 tokens, 8.6 million tokens and heads of 4 rows: the pass takes
+// 412 us; four runs of 128 tokens a warp: the same; with the log-sum-exps formed here from the
+// parts, so that the join can run beside it: 40 us more.)
 constexpr int kSumWarps = 8;
-template <int RUN>
 __global__ void __launch_bounds__(kSumWarps * 32)
 weights_kernel(const DecodeParams p, int tiles, int splits) {
-    __shared__ float4 s_sum[kSumWarps][RUN][32];
+    __shared__ float4 s_sum[kSumWarps][32];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int split = warp % splits;
-    const int tile = static_cast<int>(blockIdx.x % tiles) * (kSumWarps / splits * RUN * 128);
-    const int t0 = tile + warp / splits * (RUN * 128) + lane * 4;  // and 128 further each time
+    const int tile = static_cast<int>(blockIdx.x % tiles) * (kSumWarps / splits * 128);
+    const int t = tile + warp / splits * 128 + lane * 4;
     const int unit = static_cast<int>(blockIdx.x / tiles), hk = unit % p.a.Hkv, b = unit / p.a.Hkv;
     const int len = p.lens[b];
     if (__syncthreads_or(stopped(p.err)) || len < 0 || len > p.max_kv || tile >= len) return;
     const int G = p.a.Hq / p.a.Hkv, R = G * p.n;
-    int page[RUN];
-#pragma unroll
-    for (int k = 0; k < RUN; ++k) {
-        const int t = t0 + 128 * k;
-        page[k] = t < len && split == 0 ? p.table[static_cast<long long>(b) * p.table_stride + (t >> p.page_shift)]
-                                        : -1;
-        if (page[k] >= p.pages) page[k] = -1;  // reported by the decode kernel
-    }
-    const float* src = p.scores + static_cast<long long>(unit) * R * p.pitch + t0;
+    int page = -1;
+    if (t < len && split == 0) page = p.table[static_cast<long long>(b) * p.table_stride + (t >> p.page_shift)];
+    if (page >= p.pages) page = -1;  // reported by the decode kernel
+    const float* src = p.scores + static_cast<long long>(unit) * R * p.pitch + t;
     const float* lse = p.lse + static_cast<long long>(b) * p.n * p.a.Hq + hk * G;
-    float w[RUN][4] = {};
+    float w[4] = {};
     for (int r0 = split; r0 < R; r0 += 4 * splits) {
-        float4 x[4][RUN];
+        float4 x[4];
         float l[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int r = r0 + j * splits;
             l[j] = r < R ? lse[static_cast<long long>(r / G) * p.a.Hq + r % G] : INFINITY;
-#pragma unroll
-            for (int k = 0; k < RUN; ++k)
-                x[j][k] = r < R && t0 + 128 * k < len
-                              ? *reinterpret_cast<const float4*>(src + static_cast<long long>(r) * p.pitch + 128 * k)
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[j] = r < R && t < len ? *reinterpret_cast<const float4*>(src + static_cast<long long>(r) * p.pitch)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int k = 0; k < RUN; ++k) {
-                w[k][0] += exp2_fast(x[j][k].x - l[j]);
-                w[k][1] += exp2_fast(x[j][k].y - l[j]);
-                w[k][2] += exp2_fast(x[j][k].z - l[j]);
-                w[k][3] += exp2_fast(x[j][k].w - l[j]);
-            }
+        for (int j = 0; j < 4; ++j) {
+            w[0] += exp2_fast(x[j].x - l[j]);
+            w[1] += exp2_fast(x[j].y - l[j]);
+            w[2] += exp2_fast(x[j].z - l[j]);
+            w[3] += exp2_fast(x[j].w - l[j]);
+        }
     }
     if (splits > 1) {
-#pragma unroll
-        for (int k = 0; k < RUN; ++k)
-            s_sum[warp][k][lane] = make_float4(w[k][0], w[k][1], w[k][2], w[k][3]);
+        s_sum[warp][lane] = make_float4(w[0], w[1], w[2], w[3]);
         __syncthreads();
         if (split != 0) return;
-        for (int i = 1; i < splits; ++i)
-#pragma unroll
-            for (int k = 0; k < RUN; ++k) {
-                const float4 y = s_sum[warp + i][k][lane];
-                w[k][0] += y.x, w[k][1] += y.y, w[k][2] += y.z, w[k][3] += y.w;
-            }
-    }
-    const int old = p.fresh ? 0 : len - p.n;  // tokens before it had a sum
-#pragma unroll
-    for (int k = 0; k < RUN; ++k) {
-        if (page[k] < 0) continue;
-        const int t = t0 + 128 * k;
-        float* dst = p.weights + ((static_cast<long long>(page[k]) * p.a.Hkv + hk) << p.page_shift) +
-                     (t & ((1 << p.page_shift) - 1));
-        if (t + 4 <= old) {
-            const float4 y = *reinterpret_cast<const float4*>(dst);
-            *reinterpret_cast<float4*>(dst) =
-                make_float4(y.x + w[k][0], y.y + w[k][1], y.z + w[k][2], y.w + w[k][3]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (t + e < len) dst[e] = (t + e < old ? dst[e] : 0.f) + w[k][e];
+        for (int i = 1; i < splits; ++i) {
+            const float4 y = s_sum[warp + i][lane];
+            w[0] += y.x, w[1] += y.y, w[2] += y.z, w[3] += y.w;
         }
+    }
+    if (page < 0) return;
+    const int old = p.fresh ? 0 : len - p.n;  // tokens before it had a sum
+    float* dst = p.weights + ((static_cast<long long>(page) * p.a.Hkv + hk) << p.page_shift) +
+                 (t & ((1 << p.page_shift) - 1));
+    if (t + 4 <= old) {
+        const float4 y = *reinterpret_cast<const float4*>(dst);
+        *reinterpret_cast<float4*>(dst) = make_float4(y.x + w[0], y.y + w[1], y.z + w[2], y.w + w[3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (t + e < len) dst[e] = (t + e < old ? dst[e] : 0.f) + w[e];
     }
 }
 
@@ -500,7 +482,8 @@ cudaError_t decode(const Decode& d, cudaStream_t st) {
 // uneven sequences even out, between 128 tokens (two stages, below which the merge costs
 // more than the reads) and 2048 (where writing and reading the partial results of one tile of
 // 16 rows moves under 2% of the bytes that the part reads; each further row tile adds as much,
-// while its cache reads come from L2).
+// while its cache reads come from L2; e4m3 parts of 512, 1024 and 2048 tokens: 360, 339 and 342 us
+// for 64 sequences of up to 32768 tokens with scores kept).
 DecodePlan decode_plan(const moe_attn_shape& a, int B, int n, int max_kv, bool e8) {
     const int stage = e8 ? 128 : kTokens;
     const int row_tiles = (a.Hq / a.Hkv * n + kRowTile - 1) / kRowTile;
@@ -548,14 +531,12 @@ cudaError_t launch_decode_rest(const DecodeParams& p, cudaStream_t st) {
     if (p.weights == nullptr || p.max_kv == 0) return cudaSuccess;
     const int R = p.a.Hq / p.a.Hkv * p.n;
     const int splits = R > 16 ? 8 : R > 8 ? 4 : R > 4 ? 2 : 1;
-    const int run = kSumWarps / splits * 128;
-    const long long heads = static_cast<long long>(p.B) * p.a.Hkv;
-    const bool four = heads * (p.max_kv / (4 * run)) >= 4 * num_sms();
-    const int of = four ? 4 * run : run, tiles = (p.max_kv + of - 1) / of;
-    if (heads * tiles > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    const int of = kSumWarps / splits * 128, tiles = (p.max_kv + of - 1) / of;
+    const long long blocks = static_cast<long long>(p.B) * p.a.Hkv * tiles;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     LaunchScope ls("attention_weights", st);
-    return launch_pdl(four ? weights_kernel<4> : weights_kernel<1>, dim3(static_cast<unsigned>(heads * tiles)),
-                      dim3(kSumWarps * 32), 0, st, p, tiles, splits);
+    return launch_pdl(weights_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kSumWarps * 32), 0, st, p,
+                      tiles, splits);
 }
 
 size_t decode_ws_floats(const moe_attn_shape& a, int B, int n, int max_kv, bool e8, bool weights) {

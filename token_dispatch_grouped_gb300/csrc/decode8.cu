@@ -1,18 +1,24 @@
 // decode8.cu — attention of the newest tokens of each sequence over a paged cache of e4m3
 // values with a scale for each page and head.
 //
-// Bound by reading the cached keys and values once: 2 D bytes a token and key/value head. The
-// products are those of decode.cu (16 rows of query heads x new tokens, m16n8k16) in fp16: an
-// e4m3 value is exact in fp16, so keys and values are converted between ldmatrix and the
-// product, queries are brought to fp16's range by a power of two a row, and the scales enter
-// outside the products, the keys' at the scores and the values' at the weights. Half the bytes
-// of bf16 pages leave half the time for everything else, so
-//   - a warp takes 32 tokens of a 128-token stage (one maximum, one vote, one hand-over);
-//   - keys and values are stages of their own in the ring, freed as soon as they are read;
-//   - CTAs stay, two on an SM, and take part after part: the load warp goes on with the next
-//     part's pages while the last one's rows are merged. (With a CTA for each part: 358 us
-//     instead of MEASURED for 64 sequences of up to 32768 tokens, 32/8 heads of 128.)
-// Parts are the same for a sequence whatever else is in the batch, so its bits are too.
+// Bound by reading the cached keys and values once: 2 D bytes a token and key/value head, half
+// of what decode.cu reads, so everything else has half the time. m16n8k16 products in fp16 with
+// 16 tokens (S^T = K q^T) or 16 columns (O^T = V^T P^T) as the rows of the first operand and 8
+// query heads x new tokens as the columns of the second: grouped heads fill 8 columns sooner than
+// decode.cu's 16 rows, and the weights turn from one product's result into the other's operand
+// by movmatrix. An e4m3 value is exact in fp16, so keys and values are converted between ldmatrix
+// and the product; queries are brought to fp16's range by a power of two a row; the scales enter
+// outside the products, the keys' at the scores and the values' at the weights.
+//
+// 64 sequences of up to 32768 tokens, 32/8 heads of 128, pages of 64 (2.19 GB):
+//   decode.cu's shape (16 rows of queries, 16 tokens a warp and 64-token stage)        406 us
+//   32 tokens a warp and 128-token stages: one maximum, one vote, one hand-over for them  358
+//   8 columns of queries (about half the instructions a token); keys and values as stages
+//   of their own, freed as soon as they are read; CTAs that stay, two on an SM, and take
+//   the next part from a count in the workspace (a fixed share for each, 391 before the
+//   8 columns, is uneven: CTAs read at different rates)                               316-320
+// The last is 6.9 TB/s, 102% of the measured copy. Parts are the same for a sequence whatever
+// the lengths of the others, so its bits are too.
 #include "decode.cuh"
 
 namespace moe {

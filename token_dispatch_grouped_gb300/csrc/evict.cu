@@ -9,6 +9,13 @@
 // gather_kernel, a CTA for each new page of a head: its rows from their old pages, 2 x 2 D bytes
 // (D for e4m3) read and written a token; with e4m3 pages the new scale is the largest of the rows'
 // and the others are moved to it.
+//
+// One sequence of 32768 tokens and 8 heads (8 CTAs): select 32 us, of which about 5 for each of
+// its five sweeps over a CTA's keys (132 us with a page lookup and a load for each key and sweep);
+// 64 sequences of up to 16384 tokens: 50 us. Four copies of the bins, or twice the registers,
+// change nothing. Gather of the latter (0.93 GB) about 180 us, 5.2 TB/s: what does not depend on
+// another load comes first, as a block's chain is lengths and places -> pages -> rows and scales
+// (210 us with scales before rows and products in fp32).
 #include "attn.cuh"
 
 namespace moe {
