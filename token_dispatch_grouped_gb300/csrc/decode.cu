@@ -393,15 +393,15 @@ __global__ void __launch_bounds__(128) join_kernel(const DecodeParams p) {
 // parts, so that the join can run beside it: 40 us more.)
 constexpr int kSumWarps = 8;
 __global__ void __launch_bounds__(kSumWarps * 32)
-weights_kernel(const DecodeParams p, int tiles, int splits) {
+weights_kernel(const DecodeParams p, int tiles, int split_shift) {
     __shared__ float4 s_sum[kSumWarps][32];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int split = warp % splits;
-    const int tile = static_cast<int>(blockIdx.x % tiles) * (kSumWarps / splits * 128);
-    const int t = tile + warp / splits * 128 + lane * 4;
-    const int unit = static_cast<int>(blockIdx.x / tiles), hk = unit % p.a.Hkv, b = unit / p.a.Hkv;
+    const int splits = 1 << split_shift, split = warp & (splits - 1);
+    const int unit = static_cast<int>(blockIdx.x) / tiles, b = unit / p.a.Hkv, hk = unit - b * p.a.Hkv;
+    const int tile = (static_cast<int>(blockIdx.x) - unit * tiles) * (kSumWarps * 128 >> split_shift);
+    const int t = tile + (warp >> split_shift) * 128 + lane * 4;
     const int len = p.lens[b];
     if (__syncthreads_or(stopped(p.err)) || len < 0 || len > p.max_kv || tile >= len) return;
     const int G = p.a.Hq / p.a.Hkv, R = G * p.n;
@@ -410,16 +410,22 @@ weights_kernel(const DecodeParams p, int tiles, int splits) {
     if (page >= p.pages) page = -1;  // reported by the decode kernel
     const float* src = p.scores + static_cast<long long>(unit) * R * p.pitch + t;
     const float* lse = p.lse + static_cast<long long>(b) * p.n * p.a.Hq + hk * G;
+    const long long step = static_cast<long long>(p.pitch) << split_shift;
+    src += static_cast<long long>(split) * p.pitch;
+    int g = split % G;                                       // row r is head g of its group,
+    lse += static_cast<long long>(split / G) * p.a.Hq;       // of the token whose heads lse is at
     float w[4] = {};
     for (int r0 = split; r0 < R; r0 += 4 * splits) {
         float4 x[4];
         float l[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int r = r0 + j * splits;
-            l[j] = r < R ? lse[static_cast<long long>(r / G) * p.a.Hq + r % G] : INFINITY;
-            x[j] = r < R && t < len ? *reinterpret_cast<const float4*>(src + static_cast<long long>(r) * p.pitch)
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+            const bool row = r0 + j * splits < R;
+            l[j] = row ? lse[g] : INFINITY;
+            x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row && t < len) x[j] = *reinterpret_cast<const float4*>(src);
+            src += step;
+            for (g += splits; g >= G; g -= G) lse += p.a.Hq;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -530,13 +536,13 @@ cudaError_t launch_decode_rest(const DecodeParams& p, cudaStream_t st) {
     }
     if (p.weights == nullptr || p.max_kv == 0) return cudaSuccess;
     const int R = p.a.Hq / p.a.Hkv * p.n;
-    const int splits = R > 16 ? 8 : R > 8 ? 4 : R > 4 ? 2 : 1;
-    const int of = kSumWarps / splits * 128, tiles = (p.max_kv + of - 1) / of;
+    const int split_shift = R > 16 ? 3 : R > 8 ? 2 : R > 4 ? 1 : 0;
+    const int of = kSumWarps * 128 >> split_shift, tiles = (p.max_kv + of - 1) / of;
     const long long blocks = static_cast<long long>(p.B) * p.a.Hkv * tiles;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     LaunchScope ls("attention_weights", st);
     return launch_pdl(weights_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kSumWarps * 32), 0, st, p,
-                      tiles, splits);
+                      tiles, split_shift);
 }
 
 size_t decode_ws_floats(const moe_attn_shape& a, int B, int n, int max_kv, bool e8, bool weights) {
