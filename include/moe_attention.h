@@ -183,8 +183,8 @@ typedef struct {
  *   if the scale grew, rows 0 .. o - 1 are stored in it; the new rows are
  *   e4m3(x / scale), rounded once from fp32 (keys) or bf16 (values). A value that is
  *   not finite is stored as NaN.
- * Pages of two sequences, or twice in one, must not be the same where the call writes.
- * B <= 65535.
+ * Pages of two sequences, or twice in one, must not be the same where the call writes,
+ * nor the arrays of keys and values. B <= 65535.
  * Where cu_new does not ascend, nothing holds of what the call stores. */
 int moe_kv8_append(moe_attn_shape a, int32_t B, int32_t T, int32_t max_kv, moe_heads q,
                    moe_heads k, moe_heads v, const float* wq, const float* wk, float eps,

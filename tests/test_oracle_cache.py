@@ -84,6 +84,8 @@ def test_append8_refusals(B):
     assert app(k=_heads(B, 0, 64)) == bad and app(q_out=_heads(B, 64, 64)) == bad
     assert app(w=None) == bad and app(pos=None) == bad
     assert app(T=0) == B.MOE_OK
+    for same in (cache(), cache(v=FAKE + 4096), cache(vs=FAKE + 4096)):   # one array for both
+        assert app(c=same) == bad
 
 
 def test_decode_refusals(B):

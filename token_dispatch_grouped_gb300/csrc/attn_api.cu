@@ -544,6 +544,8 @@ int moe_kv8_append(moe_attn_shape a, int32_t B, int32_t T, int32_t max_kv, moe_h
             if (!cu_new) return MOE_ERR_INVALID_ARG;
             if (!aligned4(cu_new)) return MOE_ERR_MISALIGNED;
             ATTN_TRY(check_table(block_table, table_stride, kv_lens, max_kv, cache.page_size));
+            // keys and values are written by blocks of their own
+            if (cache.k == cache.v || cache.k_scale == cache.v_scale) return MOE_ERR_INVALID_ARG;
         }
         int* err = device_status_word();
         if (!err) return MOE_ERR_NO_DEVICE;
